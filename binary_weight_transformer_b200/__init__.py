@@ -16,6 +16,18 @@ Functions carry the ABI's names::
     y           = lowbit_linear(q, s_x, packed, s_w, fmt, N, out_dtype)
     y           = lowbit_bitlinear(x, packed, s_w, fmt, N, out_dtype, g=None, norm=NORM_RMS)
     ys          = lowbit_bitlinear_group(xs, packeds, s_ws, fmt, Ns, out_dtype)
+
+4-bit weights with one scale per group, and expert layers made of them::
+
+    packed, s_g  = lowbit_gs_pack(w, group=128, scale_dtype=F32)
+    w            = lowbit_gs_unpack(packed, s_g, K, group)
+    y            = lowbit_gs_linear(q, s_x, packed, s_g, group, out_dtype)
+    offsets, pos = lowbit_moe_plan(experts, E)
+    qs, s_xs     = lowbit_moe_gather(q, pos, s_x=s_x)
+    ys           = lowbit_gs_linear_experts(qs, s_xs, offsets, packed, s_g, group, out_dtype)
+    y            = lowbit_moe_combine(ys, pos, weights)
+    d_ys, d_w    = lowbit_moe_combine_backward(dy, ys, pos, weights)
+    dx           = lowbit_moe_combine(d_xs, pos)  # gradient of lowbit_moe_gather
 """
 from __future__ import annotations
 
@@ -29,6 +41,9 @@ FUSED_MAX_BYTES = 98304  # LOWBIT_FUSED_MAX_BYTES
 FUSED_MAX_K = 1024  # LOWBIT_FUSED_MAX_K
 GROUP_MAX = 32  # LOWBIT_GROUP_MAX
 F32, BF16, I32 = 0, 1, 2
+GS_GROUPS = (32, 64, 128, 256)  # group sizes of the group-scaled 4-bit weights
+GS_MAX_K = 1048576  # LOWBIT_GS_MAX_K
+MOE_MAX_EXPERTS = 1024  # LOWBIT_MOE_MAX_EXPERTS
 WEIGHTS_STABLE = 1  # LOWBIT_LINEAR_WEIGHTS_STABLE
 EXCLUSIVE = 2  # LOWBIT_LINEAR_EXCLUSIVE
 
@@ -70,6 +85,18 @@ ABI = {
     "lowbit_bitlinear": (_I32, [_P, _I32, _I64, _I64, _I64, _P, _I32, _F, _I32, _P, _I64, _P, _I32, _I64, _P, _I32,
                                 _I64, _P, _I64, _P, _I32, ctypes.c_uint, _P, _P]),
     "lowbit_bitlinear_group": (_I32, [_P, _I32, _I64, _I32, _I32, _F, _I32, _I32, ctypes.c_uint, _P, _P]),
+    "lowbit_gs_groups": (_I64, [_I64, _I32]),
+    "lowbit_gs_pack": (_I32, [_P, _I32, _I64, _I64, _I64, _I32, _P, _I64, _P, _I32, _I64, _P, _P]),
+    "lowbit_gs_unpack": (_I32, [_P, _I64, _P, _I32, _I64, _I64, _I64, _I32, _P, _I32, _I64, _P, _P]),
+    "lowbit_gs_linear": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I64, _P, _I32, _I64, _I32, _I64, _P, _I32, _I64,
+                                ctypes.c_uint, _P, _P]),
+    "lowbit_gs_linear_experts": (_I32, [_P, _I64, _P, _I64, _I64, _P, _I32, _P, _I64, _I64, _P, _I32, _I64, _I64,
+                                        _I32, _I64, _P, _I32, _I64, _P, _P]),
+    "lowbit_moe_plan": (_I32, [_P, _I32, _I64, _I32, _I32, _P, _P, _P, _P]),
+    "lowbit_moe_gather": (_I32, [_P, _I64, _I64, _P, _P, _I64, _I32, _P, _I64, _P, _I64, _P, _P]),
+    "lowbit_moe_combine": (_I32, [_P, _I32, _I64, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P, _P]),
+    "lowbit_moe_combine_backward": (_I32, [_P, _I64, _P, _I64, _I32, _I64, _P, _P, _I64, _I32, _I64, _P, _I64, _P,
+                                           _P, _P]),
     "lowbit_kernel_name": (ctypes.c_char_p, [_I32]),
     "lowbit_status_string": (ctypes.c_char_p, [_I32]),
     "lowbit_set_wait_limit": (_I32, [_I64]),
@@ -411,6 +438,305 @@ def lowbit_rescale(acc, s_x, s_w, fmt: int, out_dtype: int = F32, y=None, status
                               y.stride(0), _ptr(status), _stream(stream))
     _check(st, "lowbit_rescale")
     return y
+
+
+# ---------------------------------------------------------------------------
+# 4-bit weights with group scales, and expert layers
+# ---------------------------------------------------------------------------
+def _real(t, what: str) -> int:
+    """The lowbit_dtype of an fp32 or bf16 tensor."""
+    import torch
+    if t.dtype == torch.float32:
+        return F32
+    if t.dtype == torch.bfloat16:
+        return BF16
+    raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+
+
+def _real_dtype(kind: int, what: str):
+    import torch
+    if kind == F32:
+        return torch.float32
+    if kind == BF16:
+        return torch.bfloat16
+    raise ValueError(f"{what} must be F32 or BF16")
+
+
+def _takes(t, what: str, dim: int, dtype=None, device=None):
+    """The checks the C side cannot make: a CUDA tensor of this rank, type and
+    device, with unit stride along the last dimension."""
+    if t.dim() != dim:
+        raise ValueError(f"{what} must have {dim} dimension(s), got shape {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    if device is not None and t.device != device:
+        raise ValueError(f"{what} is on {t.device}, the call's other tensors on {device}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{what} must have unit stride along its last dimension")
+
+
+def _ld(t, dim: int = 0) -> int:
+    """Row stride of t: its stride along `dim`, or the row length where that
+    dimension has one entry (whose stride says nothing)."""
+    return t.stride(dim) if t.shape[dim] > 1 else max(t.stride(dim), t.shape[-1])
+
+
+def _expert_stride(t, rows: int) -> int:
+    return t.stride(0) if t.shape[0] > 1 else rows
+
+
+def _call(name: str, device, stream, *args):
+    """One ABI call with the tensors' device current and, by default, on that
+    device's current stream."""
+    import torch
+    if device.index is not None and device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(name, device, stream, *args)
+    handle = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
+    st = getattr(lib(), name)(*args, handle)
+    if st != OK:
+        raise LowbitError(st, name)
+
+
+def _status_word(status, device):
+    import torch
+    if status is not None:
+        _takes(status, "status", 1, torch.int32, device)
+    return _ptr(status)
+
+
+def gs_groups(K: int, group: int) -> int:
+    """Groups of a row of K codes; raises for a group size that is not one of GS_GROUPS."""
+    if group not in GS_GROUPS:
+        raise ValueError(f"group must be one of {GS_GROUPS}, got {group}")
+    return -(-K // group)
+
+
+def lowbit_gs_pack(w, group: int = 128, scale_dtype: int = F32, packed=None, s_g=None, ldp: int | None = None,
+                   status=None, stream=None):
+    """Quantise and pack w[N, K] (fp32 or bf16) into 4-bit codes with one
+    scale per `group` codes of a row (see lowbit.h).  Returns packed
+    [N, ldp] uint8 and s_g [N, ceil(K / group)] of the scale type."""
+    import torch
+    _takes(w, "w", 2)
+    kind = _real(w, "w")
+    N, K = w.shape
+    G = gs_groups(K, group)
+    if packed is None:
+        packed = torch.empty((N, ldp if ldp is not None else packed_ld(INT4, K)), dtype=torch.uint8, device=w.device)
+    else:
+        _takes(packed, "packed", 2, torch.uint8, w.device)
+        if packed.shape[0] != N or packed.shape[1] < packed_row_bytes(INT4, K):
+            raise ValueError(f"packed must be [{N}, >= {packed_row_bytes(INT4, K)}]")
+    if s_g is None:
+        s_g = torch.empty((N, G), dtype=_real_dtype(scale_dtype, "scale_dtype"), device=w.device)
+    else:
+        _takes(s_g, "s_g", 2, _real_dtype(scale_dtype, "scale_dtype"), w.device)
+        if tuple(s_g.shape) != (N, G):
+            raise ValueError(f"s_g must be [{N}, {G}]")
+    # the row's bytes are cleared up to the packed tensor's width, not up to
+    # the next row of a wider buffer
+    ld = _ld(packed)
+    if ld != packed.shape[1] and N > 1:
+        raise ValueError("packed must have contiguous rows: every byte of a row is written")
+    _call("lowbit_gs_pack", w.device, stream, _ptr(w), kind, N, K, _ld(w), group, _ptr(packed), ld, _ptr(s_g),
+          _real(s_g, "s_g"), _ld(s_g), _status_word(status, w.device))
+    return packed, s_g
+
+
+def _artifact(packed, s_g, K: int, group: int, dim: int, device=None):
+    import torch
+    _takes(packed, "packed", dim, torch.uint8, device)
+    _takes(s_g, "s_g", dim, None, packed.device)
+    if packed.shape[-1] < packed_row_bytes(INT4, K):
+        raise ValueError(f"packed rows hold {packed.shape[-1]} bytes, K = {K} needs {packed_row_bytes(INT4, K)}")
+    if tuple(s_g.shape) != (*packed.shape[:-1], gs_groups(K, group)):
+        raise ValueError(f"s_g must be {(*packed.shape[:-1], gs_groups(K, group))}, got {tuple(s_g.shape)}")
+    return _real(s_g, "s_g")
+
+
+def lowbit_gs_unpack(packed, s_g, K: int, group: int = 128, out_dtype: int = F32, w=None, status=None, stream=None):
+    """The values code * scale of a group-scaled artifact, [N, K]."""
+    import torch
+    kind = _artifact(packed, s_g, K, group, 2)
+    N = packed.shape[0]
+    dt = _real_dtype(out_dtype, "out_dtype")
+    if w is None:
+        w = torch.empty((N, K), dtype=dt, device=packed.device)
+    else:
+        _takes(w, "w", 2, dt, packed.device)
+        if tuple(w.shape) != (N, K):
+            raise ValueError(f"w must be [{N}, {K}]")
+    _call("lowbit_gs_unpack", packed.device, stream, _ptr(packed), _ld(packed), _ptr(s_g), kind, _ld(s_g), N, K, group,
+          _ptr(w), out_dtype, _ld(w), _status_word(status, packed.device))
+    return w
+
+
+def _token_codes(q, s_x, K):
+    import torch
+    _takes(q, "q", 2, torch.int8)
+    _takes(s_x, "s_x", 1, torch.float32, q.device)
+    K = q.shape[1] if K is None else K
+    if not 0 < K <= q.shape[1]:
+        raise ValueError(f"q rows hold {q.shape[1]} codes, K = {K}")
+    if s_x.shape[0] != q.shape[0]:
+        raise ValueError(f"s_x must be [{q.shape[0]}]")
+    return K
+
+
+def _output(y, M: int, N: int, out_dtype: int, device):
+    import torch
+    dt = _real_dtype(out_dtype, "out_dtype")
+    if y is None:
+        return torch.empty((M, N), dtype=dt, device=device)
+    _takes(y, "y", 2, dt, device)
+    if tuple(y.shape) != (M, N):
+        raise ValueError(f"y must be [{M}, {N}]")
+    return y
+
+
+def lowbit_gs_linear(q, s_x, packed, s_g, group: int = 128, out_dtype: int = F32, K: int | None = None, y=None,
+                     status=None, stream=None, weights_stable: bool = False):
+    """y[M, N] from int8 codes q[M, >=K] and a group-scaled artifact packed
+    [N, ldp], s_g [N, ceil(K / group)] (see lowbit.h); y is fp32 or bf16."""
+    K = _token_codes(q, s_x, K)
+    kind = _artifact(packed, s_g, K, group, 2, q.device)
+    M, N = q.shape[0], packed.shape[0]
+    y = _output(y, M, N, out_dtype, q.device)
+    _call("lowbit_gs_linear", q.device, stream, _ptr(q), _ld(q), _ptr(s_x), M, K, _ptr(packed), _ld(packed), _ptr(s_g),
+          kind, _ld(s_g), group, N, _ptr(y), out_dtype, _ld(y), WEIGHTS_STABLE if weights_stable else 0,
+          _status_word(status, q.device))
+    return y
+
+
+def lowbit_gs_linear_experts(q, s_x, offsets, packed, s_g, group: int = 128, out_dtype: int = F32,
+                             K: int | None = None, y=None, status=None, stream=None):
+    """lowbit_gs_linear with expert weights packed [E, N, ldp], s_g
+    [E, N, ceil(K / group)]: expert e takes rows offsets[e] .. offsets[e+1]-1
+    of q.  Rows of y behind offsets[E] are left as they were."""
+    import torch
+    K = _token_codes(q, s_x, K)
+    kind = _artifact(packed, s_g, K, group, 3, q.device)
+    E, N = packed.shape[:2]
+    _takes(offsets, "offsets", 1, torch.int32, q.device)
+    if offsets.shape[0] != E + 1:
+        raise ValueError(f"offsets must be [{E + 1}]")
+    R = q.shape[0]
+    y = _output(y, R, N, out_dtype, q.device)
+    _call("lowbit_gs_linear_experts", q.device, stream, _ptr(q), _ld(q), _ptr(s_x), R, K, _ptr(offsets), E,
+          _ptr(packed), _ld(packed, 1), _expert_stride(packed, N * _ld(packed, 1)), _ptr(s_g), kind, _ld(s_g, 1),
+          _expert_stride(s_g, N * _ld(s_g, 1)), group, N, _ptr(y), out_dtype, _ld(y), _status_word(status, q.device))
+    return y
+
+
+def lowbit_moe_plan(experts, E: int, offsets=None, pos=None, status=None, stream=None):
+    """A stable sort of the slots experts[T, k] (int32 or int64 expert ids,
+    negative: dropped) by expert.  Returns offsets [E + 1] and pos [T, k], the
+    row of each slot in expert order (-1 for a dropped one), both int32."""
+    import torch
+    _takes(experts, "experts", 2)
+    if experts.dtype not in (torch.int32, torch.int64):
+        raise TypeError(f"experts must be int32 or int64, got {experts.dtype}")
+    if not experts.is_contiguous():
+        raise ValueError("experts must be contiguous")
+    T, k = experts.shape
+    if offsets is None:
+        offsets = torch.empty(E + 1, dtype=torch.int32, device=experts.device)
+    else:
+        _takes(offsets, "offsets", 1, torch.int32, experts.device)
+        if offsets.shape[0] != E + 1:
+            raise ValueError(f"offsets must be [{E + 1}]")
+    if pos is None:
+        pos = torch.empty((T, k), dtype=torch.int32, device=experts.device)
+    else:
+        _slots(pos, "pos", torch.int32, (T, k), experts.device)
+    _call("lowbit_moe_plan", experts.device, stream, _ptr(experts), 1 if experts.dtype == torch.int64 else 0, T, k, E,
+          _ptr(offsets), _ptr(pos), _status_word(status, experts.device))
+    return offsets, pos
+
+
+def _slots(t, what: str, dtype, shape, device):
+    _takes(t, what, 2, dtype, device)
+    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous {list(shape)}")
+
+
+def lowbit_moe_gather(x, pos, s_x=None, out=None, s_out=None, status=None, stream=None):
+    """Token rows x[T, :] copied to the rows pos[T, k] of `out` (T * k rows
+    unless given; rows no slot names are left as they were), with their fp32
+    scales s_x[T] when given.  Returns out, or (out, s_out) with s_x.  The
+    gradient is lowbit_moe_combine(d_out, pos)."""
+    import torch
+    _takes(x, "x", 2)
+    T, width = x.shape
+    _slots(pos, "pos", torch.int32, (T, pos.shape[-1]), x.device)
+    if out is None:
+        out = torch.empty((pos.numel(), width), dtype=x.dtype, device=x.device)
+    else:
+        _takes(out, "out", 2, x.dtype, x.device)
+        if out.shape[1] != width:
+            raise ValueError(f"out must have rows of {width}")
+    if s_x is not None:
+        _takes(s_x, "s_x", 1, torch.float32, x.device)
+        if s_x.shape[0] != T:
+            raise ValueError(f"s_x must be [{T}]")
+        if s_out is None:
+            s_out = torch.empty(out.shape[0], dtype=torch.float32, device=x.device)
+        else:
+            _takes(s_out, "s_out", 1, torch.float32, x.device)
+            if s_out.shape[0] != out.shape[0]:
+                raise ValueError(f"s_out must be [{out.shape[0]}]")
+    elif s_out is not None:
+        raise ValueError("s_out needs s_x")
+    b = x.element_size()
+    _call("lowbit_moe_gather", x.device, stream, _ptr(x), width * b, _ld(x) * b, _ptr(s_x), _ptr(pos), T, pos.shape[1],
+          _ptr(out), _ld(out) * b, _ptr(s_out), out.shape[0], _status_word(status, x.device))
+    return out if s_x is None else (out, s_out)
+
+
+def lowbit_moe_combine(ys, pos, weights=None, y=None, status=None, stream=None):
+    """y[T, K]: for every token the sum over its slots of weights[t, j] *
+    ys[pos[t, j]] (fp32 or bf16 rows, fp32 sums); without weights the plain
+    sum, which is the gradient of lowbit_moe_gather."""
+    import torch
+    _takes(ys, "ys", 2)
+    kind = _real(ys, "ys")
+    T, k = pos.shape
+    _slots(pos, "pos", torch.int32, (T, k), ys.device)
+    if weights is not None:
+        _slots(weights, "weights", torch.float32, (T, k), ys.device)
+    y = _output(y, T, ys.shape[1], kind, ys.device)
+    _call("lowbit_moe_combine", ys.device, stream, _ptr(ys), kind, _ld(ys), ys.shape[0], _ptr(pos), _ptr(weights), T, k,
+          ys.shape[1], _ptr(y), _ld(y), _status_word(status, ys.device))
+    return y
+
+
+def lowbit_moe_combine_backward(dy, ys, pos, weights, d_ys=None, d_w=None, status=None, stream=None):
+    """Gradients of lowbit_moe_combine: d_ys like ys (rows no slot names are
+    left as they were) and d_w [T, k] fp32."""
+    import torch
+    _takes(dy, "dy", 2)
+    kind = _real(dy, "dy")
+    _takes(ys, "ys", 2, dy.dtype, dy.device)
+    T, k = pos.shape
+    K = dy.shape[1]
+    if dy.shape[0] != T or ys.shape[1] != K:
+        raise ValueError(f"dy must be [{T}, {ys.shape[1]}], got {tuple(dy.shape)}")
+    _slots(pos, "pos", torch.int32, (T, k), dy.device)
+    _slots(weights, "weights", torch.float32, (T, k), dy.device)
+    if d_ys is None:
+        d_ys = torch.empty((ys.shape[0], K), dtype=dy.dtype, device=dy.device)
+    else:
+        d_ys = _output(d_ys, ys.shape[0], K, kind, dy.device)
+    if d_w is None:
+        d_w = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+    else:
+        _slots(d_w, "d_w", torch.float32, (T, k), dy.device)
+    _call("lowbit_moe_combine_backward", dy.device, stream, _ptr(dy), _ld(dy), _ptr(ys), _ld(ys), kind, ys.shape[0],
+          _ptr(pos), _ptr(weights), T, k, K, _ptr(d_ys), _ld(d_ys), _ptr(d_w), _status_word(status, dy.device))
+    return d_ys, d_w
 
 
 def set_wait_limit(cycles: int = 0):

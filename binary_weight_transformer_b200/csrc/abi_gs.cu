@@ -1,0 +1,204 @@
+// abi_gs.cu -- the C ABI of the group-scaled 4-bit layers and of the expert
+// routing: argument checks on the host, then kernel dispatch.  Every check
+// runs before any launch.  The operators are defined in include/lowbit.h.
+#include <climits>
+
+#include "gs_internal.cuh"
+
+using namespace lowbit;
+
+namespace {
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool real_type(lowbit_dtype d) { return d == LOWBIT_F32 || d == LOWBIT_BF16; }
+
+uintptr_t size_of(lowbit_dtype d) { return d == LOWBIT_BF16 ? 2 : 4; }
+
+// log2 of a valid group, or -1
+int group_shift(int group)
+{
+    switch (group) {
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+    case 256: return 8;
+    default: return -1;
+    }
+}
+
+// Checks of a packed artifact with group scales (N rows, K codes).
+lowbit_status check_artifact(const void *packed, int64_t ldp, const void *s_g, lowbit_dtype sdt, int64_t lds, int64_t N,
+                             int64_t K, int group)
+{
+    if (packed == nullptr || s_g == nullptr || !real_type(sdt) || group_shift(group) < 0) return LOWBIT_ERR_INVALID_ARG;
+    if (N <= 0 || K <= 0 || N > INT32_MAX) return LOWBIT_ERR_INVALID_ARG;
+    if (K > LOWBIT_GS_MAX_K) return LOWBIT_ERR_UNSUPPORTED;
+    if (ldp < static_cast<int64_t>(lowbit_packed_row_bytes(LOWBIT_INT4, K)) || lds < lowbit_gs_groups(K, group))
+        return LOWBIT_ERR_INVALID_ARG;
+    if (ldp % 16 != 0 || !aligned(packed, 16) || !aligned(s_g, size_of(sdt))) return LOWBIT_ERR_ALIGNMENT;
+    return LOWBIT_OK;
+}
+
+lowbit_status check_tokens(const int8_t *q, int64_t ldq, const float *s_x, int64_t M, int64_t K, const void *y,
+                           lowbit_dtype ydt, int64_t ldy, int64_t N)
+{
+    if (q == nullptr || s_x == nullptr || y == nullptr || !real_type(ydt)) return LOWBIT_ERR_INVALID_ARG;
+    if (M <= 0 || M > INT32_MAX || ldq < K || ldy < N) return LOWBIT_ERR_INVALID_ARG;
+    if (ldq % 16 != 0 || !aligned(q, 16) || !aligned(s_x, 4) || !aligned(y, size_of(ydt))) return LOWBIT_ERR_ALIGNMENT;
+    return LOWBIT_OK;
+}
+
+lowbit_status check_slots(const void *pos, int64_t T, int k, int64_t rows)
+{
+    if (pos == nullptr || T <= 0 || k <= 0 || rows <= 0) return LOWBIT_ERR_INVALID_ARG;
+    if (T > INT32_MAX / k || rows > INT32_MAX) return LOWBIT_ERR_INVALID_ARG;
+    return aligned(pos, 4) ? LOWBIT_OK : LOWBIT_ERR_ALIGNMENT;
+}
+
+}  // namespace
+
+extern "C" {
+
+int64_t lowbit_gs_groups(int64_t K, int group)
+{
+    if (K <= 0 || group_shift(group) < 0) return 0;
+    return (K + group - 1) / group;
+}
+
+lowbit_status lowbit_gs_pack(const void *w, lowbit_dtype wdt, int64_t N, int64_t K, int64_t ldw, int group,
+                             uint8_t *packed, int64_t ldp, void *s_g, lowbit_dtype sdt, int64_t lds,
+                             int32_t *status_dev, void *stream)
+{
+    if (w == nullptr || !real_type(wdt)) return LOWBIT_ERR_INVALID_ARG;
+    const lowbit_status a = check_artifact(packed, ldp, s_g, sdt, lds, N, K, group);
+    if (a != LOWBIT_OK) return a;
+    if (ldw < K) return LOWBIT_ERR_INVALID_ARG;
+    if (!aligned(w, size_of(wdt))) return LOWBIT_ERR_ALIGNMENT;
+    const lowbit_status d = check_device();
+    if (d != LOWBIT_OK) return d;
+    const TraceRange trace("lowbit_gs_pack");
+    return gs_pack_launch(w, wdt == LOWBIT_BF16, N, K, ldw, group_shift(group), packed, ldp, s_g, sdt == LOWBIT_BF16,
+                          lds, status_dev, static_cast<cudaStream_t>(stream));
+}
+
+lowbit_status lowbit_gs_unpack(const uint8_t *packed, int64_t ldp, const void *s_g, lowbit_dtype sdt, int64_t lds,
+                               int64_t N, int64_t K, int group, void *w, lowbit_dtype wdt, int64_t ldw,
+                               int32_t *status_dev, void *stream)
+{
+    if (w == nullptr || !real_type(wdt)) return LOWBIT_ERR_INVALID_ARG;
+    const lowbit_status a = check_artifact(packed, ldp, s_g, sdt, lds, N, K, group);
+    if (a != LOWBIT_OK) return a;
+    if (ldw < K) return LOWBIT_ERR_INVALID_ARG;
+    if (!aligned(w, size_of(wdt))) return LOWBIT_ERR_ALIGNMENT;
+    const lowbit_status d = check_device();
+    if (d != LOWBIT_OK) return d;
+    const TraceRange trace("lowbit_gs_unpack");
+    return gs_unpack_launch(packed, ldp, s_g, sdt == LOWBIT_BF16, lds, N, K, group_shift(group), w, wdt == LOWBIT_BF16,
+                            ldw, status_dev, static_cast<cudaStream_t>(stream));
+}
+
+lowbit_status lowbit_gs_linear(const int8_t *q, int64_t ldq, const float *s_x, int64_t M, int64_t K,
+                               const uint8_t *packed, int64_t ldp, const void *s_g, lowbit_dtype sdt, int64_t lds,
+                               int group, int64_t N, void *y, lowbit_dtype ydt, int64_t ldy, unsigned flags,
+                               int32_t *status_dev, void *stream)
+{
+    if ((flags & ~LOWBIT_LINEAR_WEIGHTS_STABLE) != 0) return LOWBIT_ERR_INVALID_ARG;
+    lowbit_status c = check_artifact(packed, ldp, s_g, sdt, lds, N, K, group);
+    if (c == LOWBIT_OK) c = check_tokens(q, ldq, s_x, M, K, y, ydt, ldy, N);
+    if (c != LOWBIT_OK) return c;
+    const lowbit_status d = check_device();
+    if (d != LOWBIT_OK) return d;
+    const TraceRange trace("lowbit_gs_linear");
+    GsArgs a = {q, ldq, s_x, M, K, packed, ldp, 0, s_g, lds, 0, sdt == LOWBIT_BF16, group_shift(group), nullptr, 1, N, y,
+                ydt == LOWBIT_BF16, ldy, (flags & LOWBIT_LINEAR_WEIGHTS_STABLE) != 0 ? 1 : 0, status_dev};
+    return gs_mma_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+lowbit_status lowbit_gs_linear_experts(const int8_t *q, int64_t ldq, const float *s_x, int64_t rows, int64_t K,
+                                       const int32_t *offsets, int E, const uint8_t *packed, int64_t ldp,
+                                       int64_t packed_stride, const void *s_g, lowbit_dtype sdt, int64_t lds,
+                                       int64_t scale_stride, int group, int64_t N, void *y, lowbit_dtype ydt,
+                                       int64_t ldy, int32_t *status_dev, void *stream)
+{
+    if (offsets == nullptr || E <= 0 || E > LOWBIT_MOE_MAX_EXPERTS) return LOWBIT_ERR_INVALID_ARG;
+    lowbit_status c = check_artifact(packed, ldp, s_g, sdt, lds, N, K, group);
+    if (c == LOWBIT_OK) c = check_tokens(q, ldq, s_x, rows, K, y, ydt, ldy, N);
+    if (c != LOWBIT_OK) return c;
+    if (E > 1 && (packed_stride < N * ldp || scale_stride < (N - 1) * lds + lowbit_gs_groups(K, group)))
+        return LOWBIT_ERR_INVALID_ARG;
+    if (packed_stride % 16 != 0 || !aligned(offsets, 4)) return LOWBIT_ERR_ALIGNMENT;
+    const lowbit_status d = check_device();
+    if (d != LOWBIT_OK) return d;
+    const TraceRange trace("lowbit_gs_linear_experts");
+    GsArgs a = {q, ldq, s_x, rows, K, packed, ldp, packed_stride, s_g, lds, scale_stride, sdt == LOWBIT_BF16,
+                group_shift(group), offsets, E, N, y, ydt == LOWBIT_BF16, ldy, 0, status_dev};
+    return gs_mma_launch(a, static_cast<cudaStream_t>(stream));
+}
+
+lowbit_status lowbit_moe_plan(const void *experts, int experts_i64, int64_t T, int k, int E, int32_t *offsets,
+                              int32_t *pos, int32_t *status_dev, void *stream)
+{
+    if (experts == nullptr || offsets == nullptr || pos == nullptr) return LOWBIT_ERR_INVALID_ARG;
+    if (T <= 0 || k <= 0 || T > INT32_MAX / k || E <= 0 || E > LOWBIT_MOE_MAX_EXPERTS) return LOWBIT_ERR_INVALID_ARG;
+    if (!aligned(experts, experts_i64 ? 8 : 4) || !aligned(offsets, 4) || !aligned(pos, 4)) return LOWBIT_ERR_ALIGNMENT;
+    const lowbit_status d = check_device();
+    if (d != LOWBIT_OK) return d;
+    const TraceRange trace("lowbit_moe_plan");
+    return moe_plan_launch(experts, experts_i64, T * k, E, offsets, pos, status_dev, static_cast<cudaStream_t>(stream));
+}
+
+lowbit_status lowbit_moe_gather(const void *x, int64_t row_bytes, int64_t ldx_bytes, const float *s_x,
+                                const int32_t *pos, int64_t T, int k, void *out, int64_t ldo_bytes, float *s_out,
+                                int64_t rows, int32_t *status_dev, void *stream)
+{
+    if (x == nullptr || out == nullptr || row_bytes <= 0 || ldx_bytes < row_bytes || ldo_bytes < row_bytes)
+        return LOWBIT_ERR_INVALID_ARG;
+    if ((s_x == nullptr) != (s_out == nullptr)) return LOWBIT_ERR_INVALID_ARG;
+    const lowbit_status c = check_slots(pos, T, k, rows);
+    if (c != LOWBIT_OK) return c;
+    if (!aligned(s_x, 4) || !aligned(s_out, 4)) return LOWBIT_ERR_ALIGNMENT;
+    const lowbit_status d = check_device();
+    if (d != LOWBIT_OK) return d;
+    const TraceRange trace("lowbit_moe_gather");
+    return moe_gather_launch(x, row_bytes, ldx_bytes, s_x, pos, T, k, out, ldo_bytes, s_out, rows, status_dev,
+                             static_cast<cudaStream_t>(stream));
+}
+
+lowbit_status lowbit_moe_combine(const void *ys, lowbit_dtype dt, int64_t ldys, int64_t rows, const int32_t *pos,
+                                 const float *weights, int64_t T, int k, int64_t K, void *y, int64_t ldy,
+                                 int32_t *status_dev, void *stream)
+{
+    if (ys == nullptr || y == nullptr || !real_type(dt) || K <= 0 || K > INT32_MAX || ldys < K || ldy < K)
+        return LOWBIT_ERR_INVALID_ARG;
+    const lowbit_status c = check_slots(pos, T, k, rows);
+    if (c != LOWBIT_OK) return c;
+    if (!aligned(ys, size_of(dt)) || !aligned(y, size_of(dt)) || !aligned(weights, 4)) return LOWBIT_ERR_ALIGNMENT;
+    const lowbit_status d = check_device();
+    if (d != LOWBIT_OK) return d;
+    const TraceRange trace("lowbit_moe_combine");
+    return moe_combine_launch(ys, dt == LOWBIT_BF16, ldys, rows, pos, weights, T, k, K, y, ldy, status_dev,
+                              static_cast<cudaStream_t>(stream));
+}
+
+lowbit_status lowbit_moe_combine_backward(const void *dy, int64_t lddy, const void *ys, int64_t ldys, lowbit_dtype dt,
+                                          int64_t rows, const int32_t *pos, const float *weights, int64_t T, int k,
+                                          int64_t K, void *d_ys, int64_t ldd, float *d_w, int32_t *status_dev,
+                                          void *stream)
+{
+    if (dy == nullptr || ys == nullptr || weights == nullptr || d_ys == nullptr || d_w == nullptr || !real_type(dt))
+        return LOWBIT_ERR_INVALID_ARG;
+    if (K <= 0 || K > INT32_MAX || lddy < K || ldys < K || ldd < K) return LOWBIT_ERR_INVALID_ARG;
+    const lowbit_status c = check_slots(pos, T, k, rows);
+    if (c != LOWBIT_OK) return c;
+    if (!aligned(dy, size_of(dt)) || !aligned(ys, size_of(dt)) || !aligned(d_ys, size_of(dt)) || !aligned(weights, 4) ||
+        !aligned(d_w, 4))
+        return LOWBIT_ERR_ALIGNMENT;
+    const lowbit_status d = check_device();
+    if (d != LOWBIT_OK) return d;
+    const TraceRange trace("lowbit_moe_combine_backward");
+    return moe_combine_backward_launch(dy, lddy, ys, ldys, dt == LOWBIT_BF16, rows, pos, weights, T, k, K, d_ys, ldd,
+                                       d_w, status_dev, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,83 @@
+// gs_internal.cuh -- shared by the group-scaled 4-bit kernels (gs_*.cu) and
+// the routing kernels (moe_route.cu): launch arguments and scale loads.
+#pragma once
+
+#include "lowbit_internal.cuh"
+
+namespace lowbit {
+
+// One call of the group-scaled product.  Dense: offsets == nullptr, one
+// expert, token rows [0, M).  Experts: expert e owns token rows
+// [offsets[e], offsets[e+1]) of at most M rows and the weights at
+// packed + e * pstride, s_g + e * sstride (elements).
+struct GsArgs {
+    const int8_t *q;
+    int64_t ldq;
+    const float *s_x;
+    int64_t M;
+    int64_t K;
+    const uint8_t *packed;
+    int64_t ldp, pstride;
+    const void *s_g;
+    int64_t lds, sstride;
+    int s_bf16;
+    int gshift;  // log2(group)
+    const int32_t *offsets;
+    int E;
+    int64_t N;
+    void *y;
+    int y_bf16;
+    int64_t ldy;
+    int prefetch;
+    int32_t *status;
+};
+
+// Scale i of an array of fp32 or bf16 scales.  Weight-side data: the
+// read-only path, like the packed rows.
+__device__ __forceinline__ float gs_scale(const void *s, int64_t i, int is_bf16)
+{
+    if (is_bf16) {
+        uint16_t h;
+        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h) : "l"(static_cast<const uint16_t *>(s) + i));
+        return __uint_as_float(static_cast<uint32_t>(h) << 16);
+    }
+    float f;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(f) : "l"(static_cast<const float *>(s) + i));
+    return f;
+}
+
+// Token rows [lo, hi) of expert e.  The offsets are device data: a range
+// that runs backwards or past the M rows is cut to what is in bounds and
+// reported, so no row outside [0, M) is ever read or written.
+__device__ __forceinline__ void gs_expert_rows(const int32_t *offsets, int e, int64_t M, int64_t &lo, int64_t &hi,
+                                               int32_t *status)
+{
+    const int64_t a = static_cast<int32_t>(ld_act_u32(offsets + e));
+    const int64_t b = static_cast<int32_t>(ld_act_u32(offsets + e + 1));
+    lo = a < 0 ? 0 : a;
+    hi = b > M ? M : b;
+    if (a < 0 || b > M || b < a) report(status, LOWBIT_ERR_INVALID_ARG);
+    if (hi < lo) hi = lo;
+}
+
+lowbit_status gs_mma_launch(const GsArgs &a, cudaStream_t st);
+lowbit_status gs_pack_launch(const void *w, int w_bf16, int64_t N, int64_t K, int64_t ldw, int gshift, uint8_t *packed,
+                             int64_t ldp, void *s_g, int s_bf16, int64_t lds, int32_t *status, cudaStream_t st);
+lowbit_status gs_unpack_launch(const uint8_t *packed, int64_t ldp, const void *s_g, int s_bf16, int64_t lds, int64_t N,
+                               int64_t K, int gshift, void *w, int w_bf16, int64_t ldw, int32_t *status,
+                               cudaStream_t st);
+
+lowbit_status moe_plan_launch(const void *experts, int wide, int64_t slots, int E, int32_t *offsets, int32_t *pos,
+                              int32_t *status, cudaStream_t st);
+lowbit_status moe_gather_launch(const void *x, int64_t row_bytes, int64_t ldx_bytes, const float *s_x,
+                                const int32_t *pos, int64_t T, int k, void *out, int64_t ldo_bytes, float *s_out,
+                                int64_t rows, int32_t *status, cudaStream_t st);
+lowbit_status moe_combine_launch(const void *ys, int bf16, int64_t ldys, int64_t rows, const int32_t *pos,
+                                 const float *weights, int64_t T, int k, int64_t K, void *y, int64_t ldy,
+                                 int32_t *status, cudaStream_t st);
+lowbit_status moe_combine_backward_launch(const void *dy, int64_t lddy, const void *ys, int64_t ldys, int bf16,
+                                          int64_t rows, const int32_t *pos, const float *weights, int64_t T, int k,
+                                          int64_t K, void *d_ys, int64_t ldd, float *d_w, int32_t *status,
+                                          cudaStream_t st);
+
+}  // namespace lowbit

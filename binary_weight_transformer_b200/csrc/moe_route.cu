@@ -1,0 +1,494 @@
+// moe_route.cu -- token rows to expert order and back.
+//
+//   plan:     slot i = t*k + j names an expert; a stable counting sort gives
+//             pos[i], its row in expert order, and offsets[e], expert e's first row
+//   gather:   out[pos[t,j]] = x[t]
+//   combine:  y[t] = sum_j w[t,j] ys[pos[t,j]]
+//   backward: d_ys[pos[t,j]] = w[t,j] dy[t],  d_w[t,j] = <dy[t], ys[pos[t,j]]>
+//
+// All four move rows, so each is built to touch every row once: gather,
+// combine and backward run by token, which reads a token's row (x, dy) once
+// for its k slots instead of once per slot, and needs only pos.  No atomics
+// on data: every output value has one writer and a fixed order of additions.
+#include "gs_internal.cuh"
+#include "tc_common.cuh"
+
+namespace lowbit {
+namespace {
+
+// ---------------------------------------------------------------------------
+// plan
+// ---------------------------------------------------------------------------
+constexpr int kPlanCtas = 8;
+
+template <typename I>
+__device__ __forceinline__ int64_t load_expert(const void *experts, int64_t i)
+{
+    if constexpr (sizeof(I) == 4) {
+        return static_cast<int32_t>(ld_act_u32(static_cast<const int32_t *>(experts) + i));
+    } else {
+        int64_t v;
+        asm volatile("ld.global.cg.s64 %0, [%1];" : "=l"(v) : "l"(static_cast<const int64_t *>(experts) + i) : "memory");
+        return v;
+    }
+}
+
+// One cluster of C blocks.  Warp w of block r owns a contiguous segment of
+// the slots (segments ascend with r, then w).  Pass 1 counts the segment per
+// expert; the counts are turned into each warp's first row per expert (a scan
+// over warps, over blocks through distributed shared memory, and over
+// experts); pass 2 walks the segment again and places each slot.  Within 32
+// slots a match over the lanes gives the rank, so the order is the slots'.
+template <typename I>
+__global__ void __launch_bounds__(1024)
+moe_plan_kernel(const void *__restrict__ experts, int64_t slots, int E, int C, int64_t seg,
+                int32_t *__restrict__ offsets, int32_t *__restrict__ pos, int32_t *status)
+{
+    extern __shared__ int32_t sm[];
+    const int warps = blockDim.x >> 5;
+    int32_t *hist = sm;                  // [warps][E]
+    int32_t *total = sm + warps * E;     // [E] this block's counts
+    int32_t *base = total + E;           // [E] first row of this block's slots of an expert
+    __shared__ int32_t warp_sum[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = C > 1 ? static_cast<int>(tc::cluster_rank()) : 0;
+
+    for (int i = threadIdx.x; i < warps * E; i += blockDim.x) hist[i] = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+
+    const int64_t lo = (static_cast<int64_t>(rank) * warps + warp) * seg;
+    const int64_t hi = lo + seg < slots ? lo + seg : slots;
+    int32_t *mine = hist + warp * E;
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+        const int64_t i = i0 + lane;
+        int64_t e = i < hi ? load_expert<I>(experts, i) : -1;
+        if (e >= E) {
+            report(status, LOWBIT_ERR_INVALID_ARG);
+            e = -1;
+        }
+        const int key = e < 0 ? -1 : static_cast<int>(e);
+        const uint32_t peers = __match_any_sync(0xffffffffu, key);
+        if (key >= 0 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
+        __syncwarp();
+    }
+    __syncthreads();
+
+    const int e = threadIdx.x;
+    if (e < E) {
+        int32_t run = 0;
+        for (int w = 0; w < warps; ++w) {
+            const int32_t c = hist[w * E + e];
+            hist[w * E + e] = run;
+            run += c;
+        }
+        total[e] = run;
+    }
+    int32_t before = 0, all = 0;
+    if (C > 1) {
+        tc::cluster_sync_all();
+        if (e < E) {
+            for (int r = 0; r < C; ++r) {
+                int32_t c;
+                asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                             : "=r"(c) : "r"(tc::map_to_peer(tc::smem_u32(total + e), static_cast<uint32_t>(r))) : "memory");
+                if (r < rank) before += c;
+                all += c;
+            }
+        }
+        // a block may leave only when no other still reads its counts
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    } else if (e < E) {
+        all = total[e];
+    }
+    // exclusive scan of the counts over the experts
+    int32_t inc = all;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int32_t v = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += v;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    if (warp == 0) {
+        int32_t v = lane < warps ? warp_sum[lane] : 0;
+        const int32_t own = v;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        warp_sum[lane] = v - own;
+    }
+    __syncthreads();
+    if (e < E) {
+        const int32_t first = inc - all + warp_sum[warp];
+        base[e] = first + before;
+        if (rank == 0) {
+            offsets[e] = first;
+            if (e == E - 1) offsets[E] = first + all;
+        }
+    }
+    __syncthreads();
+
+    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
+        const int64_t i = i0 + lane;
+        const int64_t x = i < hi ? load_expert<I>(experts, i) : -1;
+        const int key = x < 0 || x >= E ? -1 : static_cast<int>(x);
+        const uint32_t peers = __match_any_sync(0xffffffffu, key);
+        int32_t p = -1;
+        if (key >= 0) p = base[key] + mine[key] + __popc(peers & ((1u << lane) - 1u));
+        __syncwarp();
+        if (key >= 0 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
+        __syncwarp();
+        if (i < hi) pos[i] = p;
+    }
+    if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ---------------------------------------------------------------------------
+// gather
+// ---------------------------------------------------------------------------
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kVecs = 4;  // vectors per lane and row piece
+
+template <typename V> __device__ __forceinline__ V load_vec(const V *p);
+template <> __device__ __forceinline__ uint4 load_vec(const uint4 *p) { return ld_act_u4(p); }
+template <> __device__ __forceinline__ uint32_t load_vec(const uint32_t *p) { return ld_act_u32(p); }
+template <> __device__ __forceinline__ uint16_t load_vec(const uint16_t *p) { return ld_act_u16(p); }
+template <> __device__ __forceinline__ uint8_t load_vec(const uint8_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.cg.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return static_cast<uint8_t>(v);
+}
+
+// The row of slot s, or -1: dropped slots are negative; a row past the end
+// (pos is device data) is reported and skipped.
+__device__ __forceinline__ int64_t slot_row(const int32_t *pos, int64_t s, int64_t rows, int32_t *status)
+{
+    const int64_t p = static_cast<int32_t>(ld_act_u32(pos + s));
+    if (p < rows) return p;
+    report(status, LOWBIT_ERR_INVALID_ARG);
+    return -1;
+}
+
+// A warp copies one piece (32 lanes x kVecs vectors) of a token's row to the
+// rows of its k slots.
+template <typename V>
+__global__ void __launch_bounds__(kThreads)
+moe_gather_kernel(const uint8_t *__restrict__ x, int64_t nvec, int64_t pieces, int64_t ldx, const float *__restrict__ s_x,
+                  const int32_t *__restrict__ pos, int64_t T, int k, uint8_t *__restrict__ out, int64_t ldo,
+                  float *__restrict__ s_out, int64_t rows, int32_t *status)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int64_t t = id / pieces, piece = id % pieces;
+    if (t >= T) return;
+    const V *src = reinterpret_cast<const V *>(x + t * ldx);
+    const int64_t v0 = piece * (32 * kVecs) + lane;
+    V v[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i)
+        if (v0 + 32 * i < nvec) v[i] = load_vec(src + v0 + 32 * i);
+    const float s = s_x != nullptr && piece == 0 ? ld_act_f32(s_x + t) : 0.0f;
+    for (int j = 0; j < k; ++j) {
+        const int64_t p = slot_row(pos, t * k + j, rows, status);
+        if (p < 0) continue;
+        V *dst = reinterpret_cast<V *>(out + p * ldo);
+#pragma unroll
+        for (int i = 0; i < kVecs; ++i)
+            if (v0 + 32 * i < nvec) dst[v0 + 32 * i] = v[i];
+        if (s_x != nullptr && piece == 0 && lane == 0) s_out[p] = s;
+    }
+}
+
+// ---------------------------------------------------------------------------
+// combine and its gradient
+// ---------------------------------------------------------------------------
+// kN values per vector, in fp32 registers.
+template <bool BF16, bool VEC> struct Row;
+template <> struct Row<true, true> {
+    static constexpr int kN = 8;
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw load(const void *p, int64_t at)
+    {
+        return ld_act_u4(static_cast<const uint16_t *>(p) + at);
+    }
+    static __device__ __forceinline__ float get(const Raw &r, int i)
+    {
+        const uint32_t w = (&r.x)[i >> 1];
+        return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+    }
+    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&v)[kN])
+    {
+        uint4 u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            (&u.x)[i] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = u;
+    }
+};
+template <> struct Row<false, true> {
+    static constexpr int kN = 4;
+    using Raw = uint4;
+    static __device__ __forceinline__ Raw load(const void *p, int64_t at)
+    {
+        return ld_act_u4(static_cast<const float *>(p) + at);
+    }
+    static __device__ __forceinline__ float get(const Raw &r, int i) { return __uint_as_float((&r.x)[i]); }
+    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&v)[kN])
+    {
+        *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
+    }
+};
+template <> struct Row<true, false> {
+    static constexpr int kN = 1;
+    using Raw = uint16_t;
+    static __device__ __forceinline__ Raw load(const void *p, int64_t at)
+    {
+        return ld_act_u16(static_cast<const uint16_t *>(p) + at);
+    }
+    static __device__ __forceinline__ float get(const Raw &r, int) { return __uint_as_float(static_cast<uint32_t>(r) << 16); }
+    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&v)[kN])
+    {
+        static_cast<__nv_bfloat16 *>(p)[at] = __float2bfloat16_rn(v[0]);
+    }
+};
+template <> struct Row<false, false> {
+    static constexpr int kN = 1;
+    using Raw = float;
+    static __device__ __forceinline__ Raw load(const void *p, int64_t at)
+    {
+        return ld_act_f32(static_cast<const float *>(p) + at);
+    }
+    static __device__ __forceinline__ float get(const Raw &r, int) { return r; }
+    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&v)[kN])
+    {
+        static_cast<float *>(p)[at] = v[0];
+    }
+};
+
+constexpr int kCombineVecs = 2;  // vectors per lane and row piece
+constexpr int kBatch = 4;        // slots whose loads are in flight together
+
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+moe_combine_kernel(const void *__restrict__ ys, int64_t ldys, int64_t rows, const int32_t *__restrict__ pos,
+                   const float *__restrict__ weights, int64_t T, int k, int64_t nvec, int64_t pieces,
+                   void *__restrict__ y, int64_t ldy, int32_t *status)
+{
+    using R = Row<BF16, VEC>;
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+    const int64_t t = id / pieces, piece = id % pieces;
+    if (t >= T) return;
+    const int64_t v0 = piece * (32 * kCombineVecs) + lane;
+    float acc[kCombineVecs][R::kN];
+#pragma unroll
+    for (int i = 0; i < kCombineVecs; ++i)
+#pragma unroll
+        for (int c = 0; c < R::kN; ++c) acc[i][c] = 0.0f;
+    for (int j0 = 0; j0 < k; j0 += kBatch) {
+        typename R::Raw raw[kBatch][kCombineVecs];
+        float w[kBatch];
+        bool on[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t s = t * k + j0 + b;
+            const int64_t p = j0 + b < k ? slot_row(pos, s, rows, status) : -1;
+            on[b] = p >= 0;
+            w[b] = on[b] && weights != nullptr ? ld_act_f32(weights + s) : 1.0f;
+#pragma unroll
+            for (int i = 0; i < kCombineVecs; ++i)
+                if (on[b] && v0 + 32 * i < nvec) raw[b][i] = R::load(ys, p * ldys + (v0 + 32 * i) * R::kN);
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            if (!on[b]) continue;
+#pragma unroll
+            for (int i = 0; i < kCombineVecs; ++i)
+                if (v0 + 32 * i < nvec) {
+#pragma unroll
+                    for (int c = 0; c < R::kN; ++c) acc[i][c] = __fmaf_rn(w[b], R::get(raw[b][i], c), acc[i][c]);
+                }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kCombineVecs; ++i)
+        if (v0 + 32 * i < nvec) R::store(y, t * ldy + (v0 + 32 * i) * R::kN, acc[i]);
+}
+
+// W warps of a block share a token (kWarps / W tokens per block): each takes
+// vectors lane + 32 * (warp + W * i) of the rows, kBatch slots at a time; a
+// slot's partial dots are summed over the lanes by shuffles and over the W
+// warps through shared memory, in a fixed order.
+template <bool BF16, bool VEC>
+__global__ void __launch_bounds__(kThreads)
+moe_combine_backward_kernel(const void *__restrict__ dy, int64_t lddy, const void *__restrict__ ys, int64_t ldys,
+                            int64_t rows, const int32_t *__restrict__ pos, const float *__restrict__ weights,
+                            int64_t T, int k, int64_t nvec, int W, void *__restrict__ d_ys, int64_t ldd,
+                            float *__restrict__ d_w, int32_t *status)
+{
+    using R = Row<BF16, VEC>;
+    __shared__ float part[kWarps][kBatch];
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int wt = warp % W;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kWarps / W) + warp / W;
+    for (int j0 = 0; j0 < k; j0 += kBatch) {
+        float dot[kBatch], w[kBatch];
+        int64_t p[kBatch];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int64_t s = t * k + j0 + b;
+            dot[b] = 0.0f;
+            p[b] = t < T && j0 + b < k ? slot_row(pos, s, rows, status) : -1;
+            w[b] = p[b] >= 0 ? ld_act_f32(weights + s) : 0.0f;
+        }
+        if (t < T) {
+            for (int64_t v = lane + 32 * wt; v < nvec; v += 32 * W) {
+                const typename R::Raw g = R::load(dy, t * lddy + v * R::kN);
+                typename R::Raw raw[kBatch];
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b)
+                    if (p[b] >= 0) raw[b] = R::load(ys, p[b] * ldys + v * R::kN);
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    if (p[b] < 0) continue;
+                    float o[R::kN];
+#pragma unroll
+                    for (int c = 0; c < R::kN; ++c) {
+                        const float gc = R::get(g, c);
+                        dot[b] = __fmaf_rn(gc, R::get(raw[b], c), dot[b]);
+                        o[c] = __fmul_rn(w[b], gc);
+                    }
+                    R::store(d_ys, p[b] * ldd + v * R::kN, o);
+                }
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) dot[b] += __shfl_xor_sync(0xffffffffu, dot[b], o);
+            if (lane == 0) part[warp][b] = dot[b];
+        }
+        __syncthreads();
+        if (wt == 0 && lane < kBatch && t < T && j0 + lane < k) {
+            float sum = 0.0f;
+            for (int i = 0; i < W; ++i) sum += part[warp + i][lane];
+            d_w[t * k + j0 + lane] = sum;
+        }
+        __syncthreads();
+    }
+}
+
+bool multiple_of(int64_t v, const void *a, int64_t la, const void *b, int64_t lb, int64_t n)
+{
+    return (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | static_cast<uint64_t>(la) |
+            static_cast<uint64_t>(lb) | static_cast<uint64_t>(n)) % static_cast<uint64_t>(v) == 0;
+}
+
+}  // namespace
+
+lowbit_status moe_plan_launch(const void *experts, int wide, int64_t slots, int E, int32_t *offsets, int32_t *pos,
+                              int32_t *status, cudaStream_t st)
+{
+    // One block up to 2048 slots; then as many of the eight as give every
+    // thread about two slots.
+    int C = 1;
+    while (C < kPlanCtas && slots > static_cast<int64_t>(C) * 2048) C *= 2;
+    int64_t threads = (slots + 31) / 32 * 32;
+    const int64_t need = (E + 31) / 32 * 32;
+    if (threads < need) threads = need;
+    if (threads > 1024) threads = 1024;
+    const int64_t warps = threads / 32;
+    const int64_t seg = ((slots + warps * C - 1) / (warps * C) + 31) / 32 * 32;
+    const size_t smem = static_cast<size_t>(warps + 2) * static_cast<size_t>(E) * 4;
+    auto kernel = wide ? moe_plan_kernel<int64_t> : moe_plan_kernel<int32_t>;
+    static PerDevice configured;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
+    if (configured.get(dev, [&] {
+            const int most = 34 * LOWBIT_MOE_MAX_EXPERTS * 4;
+            return cudaFuncSetAttribute(moe_plan_kernel<int64_t>, cudaFuncAttributeMaxDynamicSharedMemorySize, most) ==
+                           cudaSuccess &&
+                       cudaFuncSetAttribute(moe_plan_kernel<int32_t>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            most) == cudaSuccess
+                       ? 1
+                       : 0;
+        }) <= 0)
+        return LOWBIT_ERR_CUDA;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(C)), dim3(static_cast<unsigned>(threads)), smem, st,
+                      C > 1 ? static_cast<unsigned>(C) : 0u, experts, slots, E, C, seg, offsets, pos, status);
+}
+
+lowbit_status moe_gather_launch(const void *x, int64_t row_bytes, int64_t ldx_bytes, const float *s_x,
+                                const int32_t *pos, int64_t T, int k, void *out, int64_t ldo_bytes, float *s_out,
+                                int64_t rows, int32_t *status, cudaStream_t st)
+{
+    int64_t v = 16;
+    if (!multiple_of(16, x, ldx_bytes, out, ldo_bytes, row_bytes)) v = 4;
+    if (v == 4 && !multiple_of(4, x, ldx_bytes, out, ldo_bytes, row_bytes)) v = 2;
+    if (v == 2 && !multiple_of(2, x, ldx_bytes, out, ldo_bytes, row_bytes)) v = 1;
+    const int64_t nvec = row_bytes / v;
+    const int64_t pieces = (nvec + 32 * kVecs - 1) / (32 * kVecs);
+    const int64_t blocks = (T * pieces + kWarps - 1) / kWarps;
+    if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
+    auto kernel = v == 16  ? moe_gather_kernel<uint4>
+                  : v == 4 ? moe_gather_kernel<uint32_t>
+                  : v == 2 ? moe_gather_kernel<uint16_t>
+                           : moe_gather_kernel<uint8_t>;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, 0,
+                      static_cast<const uint8_t *>(x), nvec, pieces, ldx_bytes, s_x, pos, T, k,
+                      static_cast<uint8_t *>(out), ldo_bytes, s_out, rows, status);
+}
+
+lowbit_status moe_combine_launch(const void *ys, int bf16, int64_t ldys, int64_t rows, const int32_t *pos,
+                                 const float *weights, int64_t T, int k, int64_t K, void *y, int64_t ldy,
+                                 int32_t *status, cudaStream_t st)
+{
+    const int64_t esz = bf16 ? 2 : 4;
+    const bool vec = multiple_of(16, ys, ldys * esz, y, ldy * esz, K * esz);
+    const int64_t nvec = vec ? K * esz / 16 : K;
+    const int64_t pieces = (nvec + 32 * kCombineVecs - 1) / (32 * kCombineVecs);
+    const int64_t blocks = (T * pieces + kWarps - 1) / kWarps;
+    if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
+    auto kernel = bf16 ? (vec ? moe_combine_kernel<true, true> : moe_combine_kernel<true, false>)
+                       : (vec ? moe_combine_kernel<false, true> : moe_combine_kernel<false, false>);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, 0, ys, ldys, rows, pos,
+                      weights, T, k, nvec, pieces, y, ldy, status);
+}
+
+lowbit_status moe_combine_backward_launch(const void *dy, int64_t lddy, const void *ys, int64_t ldys, int bf16,
+                                          int64_t rows, const int32_t *pos, const float *weights, int64_t T, int k,
+                                          int64_t K, void *d_ys, int64_t ldd, float *d_w, int32_t *status,
+                                          cudaStream_t st)
+{
+    const int64_t esz = bf16 ? 2 : 4;
+    const bool vec = multiple_of(16, dy, lddy * esz, ys, ldys * esz, K * esz) &&
+                     multiple_of(16, d_ys, ldd * esz, d_ys, ldd * esz, 0);
+    const int64_t nvec = vec ? K * esz / 16 : K;
+    // Warps per token: enough for about 16 warps on every SM, and no more
+    // than the row has 32-vector pieces.
+    int W = 1;
+    while (W < kWarps && T * W < static_cast<int64_t>(device_sm_count()) * 16 && nvec > 32 * W) W *= 2;
+    const int64_t per = kWarps / W;
+    const int64_t blocks = (T + per - 1) / per;
+    if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
+    auto kernel = bf16 ? (vec ? moe_combine_backward_kernel<true, true> : moe_combine_backward_kernel<true, false>)
+                       : (vec ? moe_combine_backward_kernel<false, true> : moe_combine_backward_kernel<false, false>);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, 0, dy, lddy, ys, ldys, rows,
+                      pos, weights, T, k, nvec, W, d_ys, ldd, d_w, status);
+}
+
+}  // namespace lowbit

@@ -462,6 +462,127 @@ lowbit_status lowbit_rescale(const int32_t *acc, int64_t ldacc, int64_t M, int64
                              const float *s_w, lowbit_format f, void *y, lowbit_dtype ydt, int64_t ldy,
                              int32_t *status_dev, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * 4-bit weights with one scale per group
+ *
+ * The codes and the packed layout are those of LOWBIT_INT4 (lowbit_unpack
+ * decodes them); instead of one scale per row there is one per `group`
+ * consecutive codes of a row, group in {32, 64, 128, 256}: s_g [N, lds]
+ * fp32 or bf16 (sdt), entry (n, g) for codes g*group .. g*group + group - 1.
+ * The last group of a row may be short.  K <= LOWBIT_GS_MAX_K, else
+ * LOWBIT_ERR_UNSUPPORTED.
+ * ------------------------------------------------------------------------- */
+#define LOWBIT_GS_MAX_K 1048576
+
+/* Groups of a row, ceil(K / group); 0 for bad arguments. */
+int64_t lowbit_gs_groups(int64_t K, int group);
+
+/* lowbit_gs_pack -- quantise weights w[N,K] (fp32 or bf16, row stride ldw)
+ * and pack them:
+ *   s_g[n,g] = max_{k in g} |w[n,k]| / 7, an fp32 quotient, rounded to bf16
+ *              when sdt is LOWBIT_BF16;
+ *   c[n,k]   = the integer nearest to the exact quotient w[n,k] / s_g[n,g]
+ *              (a half goes to the even one), clipped to -7..7; a scale of 0
+ *              gives zero codes.
+ * Outputs: packed [N, ldp] (ldp >= lowbit_packed_row_bytes(LOWBIT_INT4, K), a
+ * multiple of 16, 16-byte aligned base; unowned bits of all ldp bytes written
+ * zero), s_g [N, lds], lds >= lowbit_gs_groups(K, group).  w is aligned to its
+ * element size (rows on 16-byte boundaries take vector loads).  A non-finite
+ * weight sets LOWBIT_ERR_NONFINITE in *status_dev; its group is then
+ * unspecified. */
+lowbit_status lowbit_gs_pack(const void *w, lowbit_dtype wdt, int64_t N, int64_t K, int64_t ldw, int group,
+                             uint8_t *packed, int64_t ldp, void *s_g, lowbit_dtype sdt, int64_t lds,
+                             int32_t *status_dev, void *stream);
+
+/* lowbit_gs_unpack -- the values the artifact stands for, w[n,k] = c * s_g as
+ * one fp32 product, rounded once more for a bf16 w [N, ldw].  A reserved field,
+ * or an unowned bit set in the last word of a row, sets
+ * LOWBIT_ERR_RESERVED_CODE in *status_dev; such a code decodes as 0. */
+lowbit_status lowbit_gs_unpack(const uint8_t *packed, int64_t ldp, const void *s_g, lowbit_dtype sdt, int64_t lds,
+                               int64_t N, int64_t K, int group, void *w, lowbit_dtype wdt, int64_t ldw,
+                               int32_t *status_dev, void *stream);
+
+/* lowbit_gs_linear -- lowbit_linear on such weights:
+ *   y[t,n] = s_x[t] * sum_g s_g[n,g] * acc_g,  acc_g = sum_{k in g} q[t,k] c[n,k]
+ * acc_g is exact; the sum over groups is fp32 in an order fixed by the sizes
+ * (the same call gives the same bits); y is fp32 or bf16 (LOWBIT_I32 is not
+ * possible here).  q, s_x, y and their alignments as lowbit_linear; flags: 0
+ * or LOWBIT_LINEAR_WEIGHTS_STABLE (packed and s_g). */
+lowbit_status lowbit_gs_linear(const int8_t *q, int64_t ldq, const float *s_x, int64_t M, int64_t K,
+                               const uint8_t *packed, int64_t ldp, const void *s_g, lowbit_dtype sdt, int64_t lds,
+                               int group, int64_t N, void *y, lowbit_dtype ydt, int64_t ldy, unsigned flags,
+                               int32_t *status_dev, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * Expert layers: tokens sorted by expert, every expert's product, and back
+ *
+ * Each of T tokens names k experts (k slots).  lowbit_moe_plan sorts the T*k
+ * slots by expert; lowbit_moe_gather copies token rows (int8 codes with their
+ * scales, or rows of any other type) into that order;
+ * lowbit_gs_linear_experts applies each expert's weights to its rows;
+ * lowbit_moe_combine adds the k rows of a token with its routing weights.
+ * Nothing here synchronises the host: row counts stay on the device.
+ * ------------------------------------------------------------------------- */
+#define LOWBIT_MOE_MAX_EXPERTS 1024
+
+/* lowbit_moe_plan -- a stable counting sort of the slots by expert.
+ * experts: [T, k] contiguous, int32 or (experts_i64 != 0) int64.  A negative
+ * id drops its slot; an id >= E does too and sets LOWBIT_ERR_INVALID_ARG in
+ * *status_dev.  A token may name an expert more than once.
+ *   offsets[E+1]: expert e owns rows offsets[e] .. offsets[e+1]-1, in slot
+ *                 order; offsets[E] is the number of kept slots;
+ *   pos[T,k]:     the row of each slot, -1 for a dropped one.
+ * 1 <= E <= LOWBIT_MOE_MAX_EXPERTS, T*k <= INT32_MAX. */
+lowbit_status lowbit_moe_plan(const void *experts, int experts_i64, int64_t T, int k, int E, int32_t *offsets,
+                              int32_t *pos, int32_t *status_dev, void *stream);
+
+/* lowbit_moe_gather -- out[pos[t,j]] = x[t] for every slot with pos >= 0.
+ * Rows are row_bytes bytes of any type, ldx_bytes and ldo_bytes apart; `out`
+ * holds `rows` rows, and those no slot names are left as they were.  s_x [T]
+ * and s_out [rows] fp32 are copied along, or both NULL.  A pos >= rows is
+ * skipped and sets LOWBIT_ERR_INVALID_ARG in *status_dev.  out must not
+ * overlap x.  Its gradient is lowbit_moe_combine with weights NULL. */
+lowbit_status lowbit_moe_gather(const void *x, int64_t row_bytes, int64_t ldx_bytes, const float *s_x,
+                                const int32_t *pos, int64_t T, int k, void *out, int64_t ldo_bytes, float *s_out,
+                                int64_t rows, int32_t *status_dev, void *stream);
+
+/* lowbit_gs_linear_experts -- lowbit_gs_linear with the weights of the
+ * expert that owns each row: rows offsets[e] .. offsets[e+1]-1 of q take
+ * packed + e * packed_stride (bytes, a multiple of 16) and s_g + e *
+ * scale_stride (elements).  q, s_x and y hold `rows` rows; rows of y behind
+ * offsets[E] are left as they were, as are all rows of an expert without
+ * tokens (there are none).  offsets: device int32 [E+1], ascending, within
+ * 0 .. rows; a range outside is cut to that and sets LOWBIT_ERR_INVALID_ARG in
+ * *status_dev. */
+lowbit_status lowbit_gs_linear_experts(const int8_t *q, int64_t ldq, const float *s_x, int64_t rows, int64_t K,
+                                       const int32_t *offsets, int E, const uint8_t *packed, int64_t ldp,
+                                       int64_t packed_stride, const void *s_g, lowbit_dtype sdt, int64_t lds,
+                                       int64_t scale_stride, int group, int64_t N, void *y, lowbit_dtype ydt,
+                                       int64_t ldy, int32_t *status_dev, void *stream);
+
+/* lowbit_moe_combine -- y[t] = sum_j weights[t,j] * ys[pos[t,j]] over the
+ * slots with pos >= 0: fp32 multiply-adds, j ascending, rounded once to dt
+ * (fp32 or bf16; ys and y have the same).  A token whose slots are all dropped
+ * gets zeros.  weights: fp32 [T, k] contiguous, or NULL for ones, which is the
+ * gradient of lowbit_moe_gather (ys its output's gradient).  ys holds `rows`
+ * rows; a pos >= rows is skipped and sets LOWBIT_ERR_INVALID_ARG.  K features;
+ * rows of ldys and ldy elements. */
+lowbit_status lowbit_moe_combine(const void *ys, lowbit_dtype dt, int64_t ldys, int64_t rows, const int32_t *pos,
+                                 const float *weights, int64_t T, int k, int64_t K, void *y, int64_t ldy,
+                                 int32_t *status_dev, void *stream);
+
+/* lowbit_moe_combine_backward -- from dy, the gradient of
+ * lowbit_moe_combine's y:
+ *   d_ys[pos[t,j]] = weights[t,j] * dy[t]    rounded to dt; rows of d_ys that
+ *                    no slot names are left as they were
+ *   d_w[t,j]       = sum_k dy[t,k] * ys[pos[t,j],k]   fp32; 0 for a dropped slot
+ * dy, ys and d_ys have the type dt; d_ys must not overlap dy or ys.  d_w fp32
+ * [T, k] contiguous. */
+lowbit_status lowbit_moe_combine_backward(const void *dy, int64_t lddy, const void *ys, int64_t ldys, lowbit_dtype dt,
+                                          int64_t rows, const int32_t *pos, const float *weights, int64_t T, int k,
+                                          int64_t K, void *d_ys, int64_t ldd, float *d_w, int32_t *status_dev,
+                                          void *stream);
+
 /* The kernels lowbit_linear_path can launch. */
 typedef enum {
     LOWBIT_KERNEL_GEMV = 1,           /* packed-weight GEMV (dp4a), groups of up to 4 tokens */

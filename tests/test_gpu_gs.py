@@ -1,0 +1,260 @@
+"""Group-scaled 4-bit weights on the GPU: packer, values, and the linear layer
+against their 64-bit definitions."""
+import numpy as np
+import pytest
+import torch
+
+import binary_weight_transformer_b200 as bwt
+import gs_reference as ref
+
+pytestmark = pytest.mark.gpu
+DT = {bwt.F32: torch.float32, bwt.BF16: torch.bfloat16}
+
+
+def cuda(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def status_word():
+    return torch.zeros(1, dtype=torch.int32, device="cuda")
+
+
+def weights(seed, N, K):
+    return (np.random.default_rng(seed).standard_normal((N, K)) * 0.02).astype(np.float32)
+
+
+def tokens(seed, M, K):
+    rng = np.random.default_rng(seed)
+    ld = -(-K // 16) * 16
+    q = rng.integers(-128, 128, (M, ld)).astype(np.int8)  # bytes past K are ignored: left random
+    s = (0.01 + rng.random(M)).astype(np.float32)
+    return q, s
+
+
+def check_pack(w, group, sdt, wdt=bwt.F32, ldw=None):
+    N, K = w.shape
+    t = cuda(w).to(DT[wdt])
+    w = t.float().cpu().numpy()
+    if ldw is not None:
+        wide = torch.full((N, ldw), 9.0, dtype=DT[wdt], device="cuda")
+        wide[:, :K] = t
+        t = wide[:, :K]
+    st = status_word()
+    packed, s = bwt.lowbit_gs_pack(t, group, sdt, status=st)
+    codes, scales = ref.quantise(w, group, sdt == bwt.BF16)
+    assert np.array_equal(s.float().cpu().numpy().view(np.uint32), scales.view(np.uint32))
+    assert np.array_equal(packed.cpu().numpy(), ref.pack(codes, packed.shape[1]))
+    for odt in (bwt.F32, bwt.BF16):
+        v = bwt.lowbit_gs_unpack(packed, s, K, group, odt, status=st)
+        want = codes.astype(np.float32) * np.repeat(scales, group, axis=1)[:, :K]
+        want = want if odt == bwt.F32 else ref.bf16_round(want)
+        assert np.array_equal(v.float().cpu().numpy(), want)
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("group", bwt.GS_GROUPS)
+@pytest.mark.parametrize("sdt", [bwt.F32, bwt.BF16])
+@pytest.mark.parametrize("N,K,ldw", [(1, 1, None), (3, 31, None), (5, 33, 37), (7, 256, None), (4, 1000, 1004),
+                                     (9, 1001, None), (17, 2560, 2568)])
+def test_pack_and_values(group, sdt, N, K, ldw):
+    for wdt in (bwt.F32, bwt.BF16):
+        check_pack(weights(N * K, N, K), group, sdt, wdt, ldw)
+
+
+@pytest.mark.parametrize("sdt", [bwt.F32, bwt.BF16])
+@pytest.mark.parametrize("size", [1.0, 3e-5, 1e-20, 1e-37, 3e-39, 2e-44, 3e37])
+def test_pack_halves(sdt, size):
+    """Weights on, and one step beside, every half of their group's scale, at
+    ordinary, tiny, subnormal and huge sizes."""
+    rng = np.random.default_rng(7)
+    w = np.zeros((64, 32), np.float32)
+    for n in range(64):
+        top = np.float32(size * (1 + rng.random()))
+        s = np.float32(top / np.float32(7))
+        s = ref.bf16_round(np.array([s]))[0] if sdt == bwt.BF16 else s
+        half = ((np.arange(30) % 7 + 0.5) * np.float64(s) * np.where(np.arange(30) % 2, 1, -1)).astype(np.float32)
+        step = np.arange(30) % 3
+        half = np.where(step == 1, np.nextafter(half, np.float32(np.inf)), half)
+        half = np.where(step == 2, np.nextafter(half, np.float32(-np.inf)), half)
+        w[n, 0], w[n, 1:31] = top, np.clip(half, -top, top)
+    check_pack(w, 32, sdt)
+
+
+def test_pack_zero_groups_and_signed_zero():
+    w = weights(3, 4, 512)
+    w[0] = 0.0
+    w[1, 64:128] = -0.0
+    w[2, 500:] = 0.0
+    for group in bwt.GS_GROUPS:
+        check_pack(w, group, bwt.F32)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_pack_reports_nonfinite(bad):
+    w = weights(4, 3, 300)
+    w[1, 299] = bad
+    st = status_word()
+    packed, s = bwt.lowbit_gs_pack(cuda(w), 64, status=st)
+    assert bwt.status_flags(st) == [bwt.ERR_NONFINITE]
+    codes, scales = ref.quantise(weights(4, 3, 300), 64, False)
+    assert np.array_equal(packed.cpu().numpy()[[0, 2]], ref.pack(codes, packed.shape[1])[[0, 2]])
+    assert np.array_equal(s.cpu().numpy()[:, :4], scales[:, :4])
+
+
+def test_unpack_reports_reserved_and_unowned_bits():
+    packed, s = bwt.lowbit_gs_pack(cuda(weights(5, 2, 36)), 32)
+    for byte, value in ((3, 0x08), (3, 0x80), (16, 0x10)):  # code 3, code 7, a code past K = 36
+        p = packed.clone()
+        p[1, byte] = value
+        st = status_word()
+        v = bwt.lowbit_gs_unpack(p, s, 36, 32, status=st)
+        assert bwt.status_flags(st) == [bwt.ERR_RESERVED_CODE]
+        assert torch.isfinite(v).all()
+
+
+def check_linear(M, K, N, group, sdt, odt, seed=0, stable=False, lds=None, ldy=None, ldp=None):
+    rng = np.random.default_rng(seed + M + 3 * K + 7 * N)
+    codes = rng.integers(-7, 8, (N, K)).astype(np.int8)
+    G = bwt.gs_groups(K, group)
+    scales = (0.001 + 0.01 * rng.random((N, G))).astype(np.float32)
+    if sdt == bwt.BF16:
+        scales = ref.bf16_round(scales)
+    ldp = bwt.packed_ld(bwt.INT4, K) if ldp is None else ldp
+    packed = ref.pack(codes, ldp)
+    row = bwt.packed_row_bytes(bwt.INT4, K)
+    packed[:, row:] = 0x5A  # bytes behind a row's codes carry no meaning
+    q, s_x = tokens(seed + 1, M, K)
+    s_g = cuda(scales).to(DT[sdt])
+    if lds is not None:
+        wide = torch.full((N, lds), 7.0, dtype=s_g.dtype, device="cuda")
+        wide[:, :G] = s_g
+        s_g = wide[:, :G]
+    ldy = N if ldy is None else ldy
+    y = torch.full((M, ldy), 77.0, dtype=DT[odt], device="cuda")
+    st = status_word()
+    args = (cuda(q), cuda(s_x), cuda(packed), s_g, group, odt)
+    got = bwt.lowbit_gs_linear(*args, K=K, y=y[:, :N], status=st, weights_stable=stable)
+    want, mag = ref.linear(q[:, :K], s_x, codes, scales, group)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert st.item() == 0
+    assert (err <= ref.linear_bound(want, mag, G, odt == bwt.BF16)).all().item(), err.max()
+    assert (y[:, N:] == 77.0).all()
+    again = bwt.lowbit_gs_linear(*args, K=K)
+    assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("group", bwt.GS_GROUPS)
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 33])
+@pytest.mark.parametrize("K,N", [(200, 33), (1280, 72)])
+def test_linear_few_tokens(group, M, K, N):
+    check_linear(M, K, N, group, bwt.F32 if M % 2 else bwt.BF16, bwt.F32)
+    check_linear(M, K, N, group, bwt.BF16 if M % 2 else bwt.F32, bwt.BF16)
+
+
+@pytest.mark.parametrize("group", bwt.GS_GROUPS)
+@pytest.mark.parametrize("M,K,N", [(1, 1, 1), (1, 16, 8), (2, 31, 9), (5, 127, 16), (3, 129, 5), (1, 9728, 24),
+                                   (4, 2561, 40), (16, 4097, 31)])
+def test_linear_edges(group, M, K, N):
+    check_linear(M, K, N, group, bwt.F32, bwt.F32)
+
+
+@pytest.mark.parametrize("M,K,N", [(40, 640, 96), (64, 1000, 300), (100, 2560, 200), (129, 333, 129), (300, 1280, 257),
+                                   (512, 64, 1000), (700, 2080, 136)])
+@pytest.mark.parametrize("group", bwt.GS_GROUPS)
+def test_linear_many_tokens(M, K, N, group):
+    check_linear(M, K, N, group, bwt.F32, bwt.F32)
+    check_linear(M, K, N, group, bwt.BF16, bwt.BF16)
+
+
+@pytest.mark.parametrize("M", [1, 12, 200])
+def test_linear_strides(M):
+    check_linear(M, 500, 50, 64, bwt.BF16, bwt.BF16, stable=True, lds=11, ldy=57, ldp=320)
+    check_linear(M, 512, 64, 128, bwt.F32, bwt.F32, lds=5, ldy=65, ldp=256)
+
+
+@pytest.mark.parametrize("M", [3, 16, 200])
+def test_linear_extreme_codes_and_scales(M):
+    """All codes at their limits (the largest integer sums), and scales of
+    very different sizes side by side, zeros among them."""
+    K, N, group = 2048, 40, 256
+    q = np.full((M, K), -128, np.int8)
+    codes = np.full((N, K), 7, np.int8)
+    codes[::2] = -7
+    rng = np.random.default_rng(2)
+    scales = (10.0 ** rng.integers(-30, 4, (N, K // group))).astype(np.float32)
+    scales[3] = 0.0
+    s_x = np.full(M, 0.5, np.float32)
+    packed = cuda(ref.pack(codes, K // 2))
+    got = bwt.lowbit_gs_linear(cuda(q), cuda(s_x), packed, cuda(scales), group)
+    want, mag = ref.linear(q, s_x, codes, scales, group)
+    assert (np.abs(got.double().cpu().numpy() - want) <= ref.linear_bound(want, mag, K // group, False)).all()
+    assert (got[:, 3] == 0).all()
+
+
+def test_linear_infinite_scale_stays_in_its_rows():
+    w, (q, s_x) = weights(8, 24, 256), tokens(9, 5, 256)
+    packed, s = bwt.lowbit_gs_pack(cuda(w), 64)
+    clean = bwt.lowbit_gs_linear(cuda(q), cuda(s_x), packed, s, 64)
+    s2, x2 = s.clone(), cuda(s_x)
+    s2[7, 1] = float("inf")
+    x2[3] = float("nan")
+    got = bwt.lowbit_gs_linear(cuda(q), x2, packed, s2, 64)
+    rows, cols = [0, 1, 2, 4], [n for n in range(24) if n != 7]
+    assert torch.equal(got[rows][:, cols], clean[rows][:, cols])
+    assert torch.isnan(got[3]).all() and not torch.isfinite(got[:, 7]).any()
+
+
+def test_linear_equals_int4_layer_with_one_scale():
+    """With every group scale of a row equal, the layer is lowbit_linear's
+    4-bit one: integer sums of the row times one scale."""
+    N, K, M = 96, 1024, 6
+    packed, s_w = bwt.lowbit_pack(cuda(weights(1, N, K)), bwt.INT4)
+    q, s_x = tokens(2, M, K)
+    want = bwt.lowbit_linear(cuda(q), cuda(s_x), packed, s_w, bwt.INT4, N, bwt.F32, K=K).double()
+    s_g = s_w[:, None].expand(N, K // 128).contiguous()
+    got = bwt.lowbit_gs_linear(cuda(q), cuda(s_x), packed, s_g, 128).double()
+    codes = bwt.lowbit_unpack(packed, K, bwt.INT4).cpu().numpy()
+    _, mag = ref.linear(q, s_x, codes, s_g.cpu().numpy(), 128)
+    # lowbit_linear rounds three times (conversion, scale product, product)
+    assert ((got - want).abs().cpu().numpy() <= ref.linear_bound(want.cpu().numpy(), mag, 8, False) + 3 * ref.U32 * mag).all()
+
+
+@pytest.mark.parametrize("M", [1, 16, 160])
+def test_layer_in_a_graph_and_on_another_stream(M):
+    """Prologue, product and the pack before it, captured once and replayed on
+    new inputs; and two calls at once on two streams."""
+    N, K = 264, 640
+    x = torch.randn(M, K, device="cuda")
+    w = torch.randn(N, K, device="cuda")
+
+    def layer(x, w):
+        packed, s = bwt.lowbit_gs_pack(w, 64, bwt.BF16)
+        q, s_x = bwt.lowbit_act_quant_ex(x, norm=bwt.NORM_RMS)
+        return bwt.lowbit_gs_linear(q, s_x, packed, s, 64, bwt.BF16)
+
+    eager = layer(x, w)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        layer(x, w)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = layer(x, w)
+    graph.replay()
+    assert torch.equal(out, eager)
+    x.copy_(torch.randn(M, K, device="cuda"))
+    w.copy_(torch.randn(N, K, device="cuda"))
+    graph.replay()
+    assert torch.equal(out, layer(x, w))
+
+    packed, s = bwt.lowbit_gs_pack(w, 64)
+    q, s_x = bwt.lowbit_act_quant(x)
+    want = bwt.lowbit_gs_linear(q, s_x, packed, s, 64)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], [[], []]
+    for _ in range(5):
+        for i, st in enumerate(streams):
+            got[i].append(bwt.lowbit_gs_linear(q, s_x, packed, s, 64, stream=st, y=torch.empty_like(want)))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for half in got for g in half)
