@@ -442,69 +442,114 @@ def lowbit_rescale(acc, s_x, s_w, fmt: int, out_dtype: int = F32, y=None, status
 
 # ---------------------------------------------------------------------------
 # 4-bit weights with group scales, and expert layers
+#
+# These calls take a few microseconds on the device for small inputs, so the
+# checks below are written for the host's time: one expression per tensor,
+# the current stream's handle without a Stream object (which takes 3 us), and
+# the details of a refusal worked out only when there is one.
 # ---------------------------------------------------------------------------
-def _real(t, what: str) -> int:
-    """The lowbit_dtype of an fp32 or bf16 tensor."""
-    import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+class _Torch:
+    """torch and what the calls below need of it, looked up at the first call."""
+
+    def __init__(self):
+        import torch
+        self.torch, self.empty = torch, torch.empty
+        self.i8, self.u8, self.i32, self.f32 = torch.int8, torch.uint8, torch.int32, torch.float32
+        self.kind = {torch.float32: F32, torch.bfloat16: BF16}  # lowbit_dtype of a real type
+        self.real = {F32: torch.float32, BF16: torch.bfloat16}
+        self.device = torch.cuda.current_device
+        self.stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                              lambda d: torch.cuda.current_stream(d).cuda_stream)
 
 
-def _real_dtype(kind: int, what: str):
-    import torch
-    if kind == F32:
-        return torch.float32
-    if kind == BF16:
-        return torch.bfloat16
-    raise ValueError(f"{what} must be F32 or BF16")
+_torch_names = None
 
 
-def _takes(t, what: str, dim: int, dtype=None, device=None):
+def _tt() -> _Torch:
+    global _torch_names
+    if _torch_names is None:
+        _torch_names = _Torch()
+    return _torch_names
+
+
+def _takes(t, what: str, dim: int, dtype, dev: int | None = None) -> int:
     """The checks the C side cannot make: a CUDA tensor of this rank, type and
-    device, with unit stride along the last dimension."""
-    if t.dim() != dim:
-        raise ValueError(f"{what} must have {dim} dimension(s), got shape {tuple(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor")
-    if device is not None and t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the call's other tensors on {device}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    (when given) device, with unit stride along the last dimension.  Returns
+    the device index."""
+    d = t.get_device()
+    if t.ndim != dim or t.dtype != dtype or d < 0 or (dev is not None and d != dev) or \
+            (t.stride(-1) != 1 and t.shape[-1] > 1):
+        if t.ndim != dim:
+            raise ValueError(f"{what} must have {dim} dimension(s), got shape {tuple(t.shape)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+        if d < 0:
+            raise ValueError(f"{what} must be a CUDA tensor")
+        if dev is not None and d != dev:
+            raise ValueError(f"{what} is on cuda:{d}, the call's other tensors on cuda:{dev}")
         raise ValueError(f"{what} must have unit stride along its last dimension")
+    return d
+
+
+def _kind(t, what: str) -> int:
+    """The lowbit_dtype of an fp32 or bf16 tensor."""
+    k = _tt().kind.get(t.dtype)
+    if k is None:
+        raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+    return k
+
+
+def _real(kind: int, what: str):
+    dt = _tt().real.get(kind)
+    if dt is None:
+        raise ValueError(f"{what} must be F32 or BF16")
+    return dt
 
 
 def _ld(t, dim: int = 0) -> int:
-    """Row stride of t: its stride along `dim`, or the row length where that
-    dimension has one entry (whose stride says nothing)."""
+    """Row stride of t: its stride along `dim`, or at least the row length
+    where that dimension has one entry (whose stride says nothing)."""
     return t.stride(dim) if t.shape[dim] > 1 else max(t.stride(dim), t.shape[-1])
 
 
-def _expert_stride(t, rows: int) -> int:
-    return t.stride(0) if t.shape[0] > 1 else rows
+def _slots(t, what: str, dtype, T: int, k: int, dev: int):
+    _takes(t, what, 2, dtype, dev)
+    if t.shape[0] != T or t.shape[1] != k or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous [{T}, {k}], got {tuple(t.shape)}")
 
 
-def _call(name: str, device, stream, *args):
+def _output(y, what: str, rows: int, cols: int, kind: int, dev: int):
+    dt = _real(kind, "the output type")
+    if y is None:
+        return _tt().empty((rows, cols), dtype=dt, device=dev)
+    _takes(y, what, 2, dt, dev)
+    if y.shape[0] != rows or y.shape[1] != cols:
+        raise ValueError(f"{what} must be [{rows}, {cols}], got {tuple(y.shape)}")
+    return y
+
+
+def _vector(t, what: str, n: int, dtype, dev: int):
+    if t is None:
+        return _tt().empty(n, dtype=dtype, device=dev)
+    _takes(t, what, 1, dtype, dev)
+    if t.shape[0] != n:
+        raise ValueError(f"{what} must be [{n}], got {tuple(t.shape)}")
+    return t
+
+
+def _call(name: str, dev: int, status, stream, *args):
     """One ABI call with the tensors' device current and, by default, on that
     device's current stream."""
-    import torch
-    if device.index is not None and device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
-            return _call(name, device, stream, *args)
-    handle = torch.cuda.current_stream().cuda_stream if stream is None else stream.cuda_stream
-    st = getattr(lib(), name)(*args, handle)
+    tt = _tt()
+    if tt.device() != dev:
+        with tt.torch.cuda.device(dev):
+            return _call(name, dev, status, stream, *args)
+    if status is not None:
+        _takes(status, "status", 1, tt.i32, dev)
+        status = status.data_ptr()
+    st = getattr(_lib or lib(), name)(*args, status, tt.stream(dev) if stream is None else stream.cuda_stream)
     if st != OK:
         raise LowbitError(st, name)
-
-
-def _status_word(status, device):
-    import torch
-    if status is not None:
-        _takes(status, "status", 1, torch.int32, device)
-    return _ptr(status)
 
 
 def gs_groups(K: int, group: int) -> int:
@@ -518,96 +563,75 @@ def lowbit_gs_pack(w, group: int = 128, scale_dtype: int = F32, packed=None, s_g
                    status=None, stream=None):
     """Quantise and pack w[N, K] (fp32 or bf16) into 4-bit codes with one
     scale per `group` codes of a row (see lowbit.h).  Returns packed
-    [N, ldp] uint8 and s_g [N, ceil(K / group)] of the scale type."""
-    import torch
-    _takes(w, "w", 2)
-    kind = _real(w, "w")
+    [N, ldp] uint8 and s_g [N, ceil(K / group)] of the scale type.  Every
+    byte of a packed row is written, so rows must be contiguous."""
+    kind = _kind(w, "w")
+    dev = _takes(w, "w", 2, w.dtype)
     N, K = w.shape
     G = gs_groups(K, group)
+    tt = _tt()
     if packed is None:
-        packed = torch.empty((N, ldp if ldp is not None else packed_ld(INT4, K)), dtype=torch.uint8, device=w.device)
+        packed = tt.empty((N, ldp if ldp is not None else (K + 31) // 32 * 16), dtype=tt.u8, device=dev)
     else:
-        _takes(packed, "packed", 2, torch.uint8, w.device)
-        if packed.shape[0] != N or packed.shape[1] < packed_row_bytes(INT4, K):
-            raise ValueError(f"packed must be [{N}, >= {packed_row_bytes(INT4, K)}]")
-    if s_g is None:
-        s_g = torch.empty((N, G), dtype=_real_dtype(scale_dtype, "scale_dtype"), device=w.device)
-    else:
-        _takes(s_g, "s_g", 2, _real_dtype(scale_dtype, "scale_dtype"), w.device)
-        if tuple(s_g.shape) != (N, G):
-            raise ValueError(f"s_g must be [{N}, {G}]")
-    # the row's bytes are cleared up to the packed tensor's width, not up to
-    # the next row of a wider buffer
-    ld = _ld(packed)
-    if ld != packed.shape[1] and N > 1:
-        raise ValueError("packed must have contiguous rows: every byte of a row is written")
-    _call("lowbit_gs_pack", w.device, stream, _ptr(w), kind, N, K, _ld(w), group, _ptr(packed), ld, _ptr(s_g),
-          _real(s_g, "s_g"), _ld(s_g), _status_word(status, w.device))
+        _takes(packed, "packed", 2, tt.u8, dev)
+        if packed.shape[0] != N or not packed.is_contiguous():
+            raise ValueError(f"packed must be contiguous with {N} rows")
+    s_g = _output(s_g, "s_g", N, G, scale_dtype, dev)
+    _call("lowbit_gs_pack", dev, status, stream, w.data_ptr(), kind, N, K, _ld(w), group, packed.data_ptr(),
+          packed.shape[1], s_g.data_ptr(), scale_dtype, _ld(s_g))
     return packed, s_g
 
 
-def _artifact(packed, s_g, K: int, group: int, dim: int, device=None):
-    import torch
-    _takes(packed, "packed", dim, torch.uint8, device)
-    _takes(s_g, "s_g", dim, None, packed.device)
-    if packed.shape[-1] < packed_row_bytes(INT4, K):
-        raise ValueError(f"packed rows hold {packed.shape[-1]} bytes, K = {K} needs {packed_row_bytes(INT4, K)}")
-    if tuple(s_g.shape) != (*packed.shape[:-1], gs_groups(K, group)):
-        raise ValueError(f"s_g must be {(*packed.shape[:-1], gs_groups(K, group))}, got {tuple(s_g.shape)}")
-    return _real(s_g, "s_g")
+def _artifact(packed, s_g, K: int, group: int, dim: int, dev: int) -> int:
+    """Checks of an artifact and its scales (rows, or experts and rows, in
+    front); the scales' lowbit_dtype."""
+    kind = _kind(s_g, "s_g")
+    _takes(packed, "packed", dim, _tt().u8, dev)
+    _takes(s_g, "s_g", dim, s_g.dtype, dev)
+    p, s = packed.shape, s_g.shape
+    if p[-1] < (K + 7) // 8 * 4:
+        raise ValueError(f"packed rows hold {p[-1]} bytes, K = {K} needs {(K + 7) // 8 * 4}")
+    if s[-1] != gs_groups(K, group) or s[:-1] != p[:-1]:
+        raise ValueError(f"s_g must be {(*p[:-1], gs_groups(K, group))}, got {tuple(s)}")
+    return kind
 
 
 def lowbit_gs_unpack(packed, s_g, K: int, group: int = 128, out_dtype: int = F32, w=None, status=None, stream=None):
     """The values code * scale of a group-scaled artifact, [N, K]."""
-    import torch
-    kind = _artifact(packed, s_g, K, group, 2)
+    dev = packed.get_device()
+    kind = _artifact(packed, s_g, K, group, 2, dev)
     N = packed.shape[0]
-    dt = _real_dtype(out_dtype, "out_dtype")
-    if w is None:
-        w = torch.empty((N, K), dtype=dt, device=packed.device)
-    else:
-        _takes(w, "w", 2, dt, packed.device)
-        if tuple(w.shape) != (N, K):
-            raise ValueError(f"w must be [{N}, {K}]")
-    _call("lowbit_gs_unpack", packed.device, stream, _ptr(packed), _ld(packed), _ptr(s_g), kind, _ld(s_g), N, K, group,
-          _ptr(w), out_dtype, _ld(w), _status_word(status, packed.device))
+    w = _output(w, "w", N, K, out_dtype, dev)
+    _call("lowbit_gs_unpack", dev, status, stream, packed.data_ptr(), _ld(packed), s_g.data_ptr(), kind, _ld(s_g), N, K,
+          group, w.data_ptr(), out_dtype, _ld(w))
     return w
 
 
 def _token_codes(q, s_x, K):
-    import torch
-    _takes(q, "q", 2, torch.int8)
-    _takes(s_x, "s_x", 1, torch.float32, q.device)
-    K = q.shape[1] if K is None else K
-    if not 0 < K <= q.shape[1]:
-        raise ValueError(f"q rows hold {q.shape[1]} codes, K = {K}")
-    if s_x.shape[0] != q.shape[0]:
-        raise ValueError(f"s_x must be [{q.shape[0]}]")
-    return K
-
-
-def _output(y, M: int, N: int, out_dtype: int, device):
-    import torch
-    dt = _real_dtype(out_dtype, "out_dtype")
-    if y is None:
-        return torch.empty((M, N), dtype=dt, device=device)
-    _takes(y, "y", 2, dt, device)
-    if tuple(y.shape) != (M, N):
-        raise ValueError(f"y must be [{M}, {N}]")
-    return y
+    tt = _tt()
+    dev = _takes(q, "q", 2, tt.i8)
+    _takes(s_x, "s_x", 1, tt.f32, dev)
+    M, width = q.shape
+    if K is None:
+        K = width
+    if not 0 < K <= width:
+        raise ValueError(f"q rows hold {width} codes, K = {K}")
+    if s_x.shape[0] != M:
+        raise ValueError(f"s_x must be [{M}], got {tuple(s_x.shape)}")
+    return dev, M, K
 
 
 def lowbit_gs_linear(q, s_x, packed, s_g, group: int = 128, out_dtype: int = F32, K: int | None = None, y=None,
                      status=None, stream=None, weights_stable: bool = False):
     """y[M, N] from int8 codes q[M, >=K] and a group-scaled artifact packed
     [N, ldp], s_g [N, ceil(K / group)] (see lowbit.h); y is fp32 or bf16."""
-    K = _token_codes(q, s_x, K)
-    kind = _artifact(packed, s_g, K, group, 2, q.device)
-    M, N = q.shape[0], packed.shape[0]
-    y = _output(y, M, N, out_dtype, q.device)
-    _call("lowbit_gs_linear", q.device, stream, _ptr(q), _ld(q), _ptr(s_x), M, K, _ptr(packed), _ld(packed), _ptr(s_g),
-          kind, _ld(s_g), group, N, _ptr(y), out_dtype, _ld(y), WEIGHTS_STABLE if weights_stable else 0,
-          _status_word(status, q.device))
+    dev, M, K = _token_codes(q, s_x, K)
+    kind = _artifact(packed, s_g, K, group, 2, dev)
+    N = packed.shape[0]
+    y = _output(y, "y", M, N, out_dtype, dev)
+    _call("lowbit_gs_linear", dev, status, stream, q.data_ptr(), _ld(q), s_x.data_ptr(), M, K, packed.data_ptr(),
+          _ld(packed), s_g.data_ptr(), kind, _ld(s_g), group, N, y.data_ptr(), out_dtype, _ld(y),
+          WEIGHTS_STABLE if weights_stable else 0)
     return y
 
 
@@ -616,18 +640,15 @@ def lowbit_gs_linear_experts(q, s_x, offsets, packed, s_g, group: int = 128, out
     """lowbit_gs_linear with expert weights packed [E, N, ldp], s_g
     [E, N, ceil(K / group)]: expert e takes rows offsets[e] .. offsets[e+1]-1
     of q.  Rows of y behind offsets[E] are left as they were."""
-    import torch
-    K = _token_codes(q, s_x, K)
-    kind = _artifact(packed, s_g, K, group, 3, q.device)
+    dev, R, K = _token_codes(q, s_x, K)
+    kind = _artifact(packed, s_g, K, group, 3, dev)
     E, N = packed.shape[:2]
-    _takes(offsets, "offsets", 1, torch.int32, q.device)
-    if offsets.shape[0] != E + 1:
-        raise ValueError(f"offsets must be [{E + 1}]")
-    R = q.shape[0]
-    y = _output(y, R, N, out_dtype, q.device)
-    _call("lowbit_gs_linear_experts", q.device, stream, _ptr(q), _ld(q), _ptr(s_x), R, K, _ptr(offsets), E,
-          _ptr(packed), _ld(packed, 1), _expert_stride(packed, N * _ld(packed, 1)), _ptr(s_g), kind, _ld(s_g, 1),
-          _expert_stride(s_g, N * _ld(s_g, 1)), group, N, _ptr(y), out_dtype, _ld(y), _status_word(status, q.device))
+    _vector(offsets, "offsets", E + 1, _tt().i32, dev)
+    y = _output(y, "y", R, N, out_dtype, dev)
+    ldp, lds = _ld(packed, 1), _ld(s_g, 1)
+    _call("lowbit_gs_linear_experts", dev, status, stream, q.data_ptr(), _ld(q), s_x.data_ptr(), R, K,
+          offsets.data_ptr(), E, packed.data_ptr(), ldp, packed.stride(0) if E > 1 else N * ldp, s_g.data_ptr(), kind,
+          lds, s_g.stride(0) if E > 1 else N * lds, group, N, y.data_ptr(), out_dtype, _ld(y))
     return y
 
 
@@ -635,32 +656,22 @@ def lowbit_moe_plan(experts, E: int, offsets=None, pos=None, status=None, stream
     """A stable sort of the slots experts[T, k] (int32 or int64 expert ids,
     negative: dropped) by expert.  Returns offsets [E + 1] and pos [T, k], the
     row of each slot in expert order (-1 for a dropped one), both int32."""
-    import torch
-    _takes(experts, "experts", 2)
-    if experts.dtype not in (torch.int32, torch.int64):
+    tt = _tt()
+    wide = experts.dtype != tt.i32
+    if wide and experts.dtype != tt.torch.int64:
         raise TypeError(f"experts must be int32 or int64, got {experts.dtype}")
+    dev = _takes(experts, "experts", 2, experts.dtype)
     if not experts.is_contiguous():
         raise ValueError("experts must be contiguous")
     T, k = experts.shape
-    if offsets is None:
-        offsets = torch.empty(E + 1, dtype=torch.int32, device=experts.device)
-    else:
-        _takes(offsets, "offsets", 1, torch.int32, experts.device)
-        if offsets.shape[0] != E + 1:
-            raise ValueError(f"offsets must be [{E + 1}]")
+    offsets = _vector(offsets, "offsets", E + 1, tt.i32, dev)
     if pos is None:
-        pos = torch.empty((T, k), dtype=torch.int32, device=experts.device)
+        pos = tt.empty((T, k), dtype=tt.i32, device=dev)
     else:
-        _slots(pos, "pos", torch.int32, (T, k), experts.device)
-    _call("lowbit_moe_plan", experts.device, stream, _ptr(experts), 1 if experts.dtype == torch.int64 else 0, T, k, E,
-          _ptr(offsets), _ptr(pos), _status_word(status, experts.device))
+        _slots(pos, "pos", tt.i32, T, k, dev)
+    _call("lowbit_moe_plan", dev, status, stream, experts.data_ptr(), 1 if wide else 0, T, k, E, offsets.data_ptr(),
+          pos.data_ptr())
     return offsets, pos
-
-
-def _slots(t, what: str, dtype, shape, device):
-    _takes(t, what, 2, dtype, device)
-    if tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous {list(shape)}")
 
 
 def lowbit_moe_gather(x, pos, s_x=None, out=None, s_out=None, status=None, stream=None):
@@ -668,31 +679,26 @@ def lowbit_moe_gather(x, pos, s_x=None, out=None, s_out=None, status=None, strea
     unless given; rows no slot names are left as they were), with their fp32
     scales s_x[T] when given.  Returns out, or (out, s_out) with s_x.  The
     gradient is lowbit_moe_combine(d_out, pos)."""
-    import torch
-    _takes(x, "x", 2)
+    tt = _tt()
+    dev = _takes(x, "x", 2, x.dtype)
     T, width = x.shape
-    _slots(pos, "pos", torch.int32, (T, pos.shape[-1]), x.device)
+    k = pos.shape[-1]
+    _slots(pos, "pos", tt.i32, T, k, dev)
     if out is None:
-        out = torch.empty((pos.numel(), width), dtype=x.dtype, device=x.device)
+        out = tt.empty((T * k, width), dtype=x.dtype, device=dev)
     else:
-        _takes(out, "out", 2, x.dtype, x.device)
+        _takes(out, "out", 2, x.dtype, dev)
         if out.shape[1] != width:
-            raise ValueError(f"out must have rows of {width}")
+            raise ValueError(f"out must have rows of {width}, got {tuple(out.shape)}")
+    rows = out.shape[0]
     if s_x is not None:
-        _takes(s_x, "s_x", 1, torch.float32, x.device)
-        if s_x.shape[0] != T:
-            raise ValueError(f"s_x must be [{T}]")
-        if s_out is None:
-            s_out = torch.empty(out.shape[0], dtype=torch.float32, device=x.device)
-        else:
-            _takes(s_out, "s_out", 1, torch.float32, x.device)
-            if s_out.shape[0] != out.shape[0]:
-                raise ValueError(f"s_out must be [{out.shape[0]}]")
+        _vector(s_x, "s_x", T, tt.f32, dev)
+        s_out = _vector(s_out, "s_out", rows, tt.f32, dev)
     elif s_out is not None:
         raise ValueError("s_out needs s_x")
     b = x.element_size()
-    _call("lowbit_moe_gather", x.device, stream, _ptr(x), width * b, _ld(x) * b, _ptr(s_x), _ptr(pos), T, pos.shape[1],
-          _ptr(out), _ld(out) * b, _ptr(s_out), out.shape[0], _status_word(status, x.device))
+    _call("lowbit_moe_gather", dev, status, stream, x.data_ptr(), width * b, _ld(x) * b, _ptr(s_x), pos.data_ptr(), T,
+          k, out.data_ptr(), _ld(out) * b, _ptr(s_out), rows)
     return out if s_x is None else (out, s_out)
 
 
@@ -700,42 +706,39 @@ def lowbit_moe_combine(ys, pos, weights=None, y=None, status=None, stream=None):
     """y[T, K]: for every token the sum over its slots of weights[t, j] *
     ys[pos[t, j]] (fp32 or bf16 rows, fp32 sums); without weights the plain
     sum, which is the gradient of lowbit_moe_gather."""
-    import torch
-    _takes(ys, "ys", 2)
-    kind = _real(ys, "ys")
+    tt = _tt()
+    kind = _kind(ys, "ys")
+    dev = _takes(ys, "ys", 2, ys.dtype)
+    R, K = ys.shape
     T, k = pos.shape
-    _slots(pos, "pos", torch.int32, (T, k), ys.device)
+    _slots(pos, "pos", tt.i32, T, k, dev)
     if weights is not None:
-        _slots(weights, "weights", torch.float32, (T, k), ys.device)
-    y = _output(y, T, ys.shape[1], kind, ys.device)
-    _call("lowbit_moe_combine", ys.device, stream, _ptr(ys), kind, _ld(ys), ys.shape[0], _ptr(pos), _ptr(weights), T, k,
-          ys.shape[1], _ptr(y), _ld(y), _status_word(status, ys.device))
+        _slots(weights, "weights", tt.f32, T, k, dev)
+    y = _output(y, "y", T, K, kind, dev)
+    _call("lowbit_moe_combine", dev, status, stream, ys.data_ptr(), kind, _ld(ys), R, pos.data_ptr(), _ptr(weights), T,
+          k, K, y.data_ptr(), _ld(y))
     return y
 
 
 def lowbit_moe_combine_backward(dy, ys, pos, weights, d_ys=None, d_w=None, status=None, stream=None):
     """Gradients of lowbit_moe_combine: d_ys like ys (rows no slot names are
     left as they were) and d_w [T, k] fp32."""
-    import torch
-    _takes(dy, "dy", 2)
-    kind = _real(dy, "dy")
-    _takes(ys, "ys", 2, dy.dtype, dy.device)
-    T, k = pos.shape
-    K = dy.shape[1]
-    if dy.shape[0] != T or ys.shape[1] != K:
-        raise ValueError(f"dy must be [{T}, {ys.shape[1]}], got {tuple(dy.shape)}")
-    _slots(pos, "pos", torch.int32, (T, k), dy.device)
-    _slots(weights, "weights", torch.float32, (T, k), dy.device)
-    if d_ys is None:
-        d_ys = torch.empty((ys.shape[0], K), dtype=dy.dtype, device=dy.device)
-    else:
-        d_ys = _output(d_ys, ys.shape[0], K, kind, dy.device)
+    tt = _tt()
+    kind = _kind(dy, "dy")
+    dev = _takes(dy, "dy", 2, dy.dtype)
+    _takes(ys, "ys", 2, dy.dtype, dev)
+    (T, k), (R, K) = pos.shape, ys.shape
+    if dy.shape[0] != T or dy.shape[1] != K:
+        raise ValueError(f"dy must be [{T}, {K}], got {tuple(dy.shape)}")
+    _slots(pos, "pos", tt.i32, T, k, dev)
+    _slots(weights, "weights", tt.f32, T, k, dev)
+    d_ys = _output(d_ys, "d_ys", R, K, kind, dev)
     if d_w is None:
-        d_w = torch.empty((T, k), dtype=torch.float32, device=dy.device)
+        d_w = tt.empty((T, k), dtype=tt.f32, device=dev)
     else:
-        _slots(d_w, "d_w", torch.float32, (T, k), dy.device)
-    _call("lowbit_moe_combine_backward", dy.device, stream, _ptr(dy), _ld(dy), _ptr(ys), _ld(ys), kind, ys.shape[0],
-          _ptr(pos), _ptr(weights), T, k, K, _ptr(d_ys), _ld(d_ys), _ptr(d_w), _status_word(status, dy.device))
+        _slots(d_w, "d_w", tt.f32, T, k, dev)
+    _call("lowbit_moe_combine_backward", dev, status, stream, dy.data_ptr(), _ld(dy), ys.data_ptr(), _ld(ys), kind, R,
+          pos.data_ptr(), weights.data_ptr(), T, k, K, d_ys.data_ptr(), _ld(d_ys), d_w.data_ptr())
     return d_ys, d_w
 
 
