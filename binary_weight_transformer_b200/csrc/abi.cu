@@ -72,6 +72,7 @@ lowbit_status rescale_launch(const int32_t *acc, int64_t ldacc, int64_t M, int64
 lowbit_status set_wait_limit_gemm(long long cycles);
 lowbit_status set_wait_limit_gemm_ts(long long cycles);
 lowbit_status set_wait_limit_skinny(long long cycles);
+lowbit_status set_wait_limit_gs(long long cycles);
 
 lowbit_status launch_status()
 {
@@ -623,6 +624,7 @@ lowbit_status lowbit_set_wait_limit(int64_t cycles)
     lowbit_status s = set_wait_limit_gemm(c);
     if (s == LOWBIT_OK) s = set_wait_limit_gemm_ts(c);
     if (s == LOWBIT_OK) s = set_wait_limit_skinny(c);
+    if (s == LOWBIT_OK) s = set_wait_limit_gs(c);
     return s;
 }
 

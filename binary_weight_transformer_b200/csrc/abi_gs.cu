@@ -56,6 +56,14 @@ lowbit_status check_slots(const void *pos, int64_t T, int k, int64_t rows)
     return aligned(pos, 4) ? LOWBIT_OK : LOWBIT_ERR_ALIGNMENT;
 }
 
+// The kernel for a call: the warp-level one for few rows (per expert, on
+// average), the tcgen05 one for many.
+lowbit_status gs_product(const GsArgs &a, cudaStream_t st)
+{
+    const int64_t rows = a.offsets != nullptr ? a.M / a.E : a.M;
+    return rows <= 64 ? gs_mma_launch(a, st) : gs_gemm_launch(a, st);
+}
+
 }  // namespace
 
 extern "C" {
@@ -112,7 +120,7 @@ lowbit_status lowbit_gs_linear(const int8_t *q, int64_t ldq, const float *s_x, i
     const TraceRange trace("lowbit_gs_linear");
     GsArgs a = {q, ldq, s_x, M, K, packed, ldp, 0, s_g, lds, 0, sdt == LOWBIT_BF16, group_shift(group), nullptr, 1, N, y,
                 ydt == LOWBIT_BF16, ldy, (flags & LOWBIT_LINEAR_WEIGHTS_STABLE) != 0 ? 1 : 0, status_dev};
-    return gs_mma_launch(a, static_cast<cudaStream_t>(stream));
+    return gs_product(a, static_cast<cudaStream_t>(stream));
 }
 
 lowbit_status lowbit_gs_linear_experts(const int8_t *q, int64_t ldq, const float *s_x, int64_t rows, int64_t K,
@@ -133,7 +141,7 @@ lowbit_status lowbit_gs_linear_experts(const int8_t *q, int64_t ldq, const float
     const TraceRange trace("lowbit_gs_linear_experts");
     GsArgs a = {q, ldq, s_x, rows, K, packed, ldp, packed_stride, s_g, lds, scale_stride, sdt == LOWBIT_BF16,
                 group_shift(group), offsets, E, N, y, ydt == LOWBIT_BF16, ldy, 0, status_dev};
-    return gs_mma_launch(a, static_cast<cudaStream_t>(stream));
+    return gs_product(a, static_cast<cudaStream_t>(stream));
 }
 
 lowbit_status lowbit_moe_plan(const void *experts, int experts_i64, int64_t T, int k, int E, int32_t *offsets,

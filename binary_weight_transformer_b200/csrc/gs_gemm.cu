@@ -1,0 +1,493 @@
+// gs_gemm.cu -- the group-scaled 4-bit product for many tokens, on SM pairs
+// (tcgen05 cta_group::2, int8), dense or by expert.
+//
+//   y[t,n] = s_x[t] * sum_g s_g[n,g] * acc_g[t,n],  acc_g = sum_{k in g} q[t,k] c[n,k]
+//
+// A scale per group keeps the integer sums from running over all of K: each
+// group's sum has to leave the tensor core, be converted and added in fp32.
+// The operands are therefore placed so that this costs least: the MMA's A
+// operand is a 256-row tile of weight codes and B a tile of NT tokens, so a
+// lane of tensor memory is a weight row, and a group's scale is ONE value per
+// thread for all the columns it drains: one conversion and half a packed
+// multiply-add per element, no loads.  The running fp32 sums of a 128 x NT
+// half tile stay in the registers of 256 threads (NT / 2 each).  The two
+// accumulator buffers (2 x NT columns) let the MMAs of one group run while
+// the previous one is drained.
+//
+// A cluster of two CTAs computes a tile of 256 weight rows x NT tokens.  CTA r
+// stages its 128 rows' packed codes and its half of the tokens with TMA,
+// expands the codes (c << 4) into its own shared memory (the rows of A it
+// owns) and drains its own 128 lanes.  The even CTA issues the MMAs.
+//
+// Warps (512 threads): 0 TMA, 1 MMA issue and tensor memory, 2-3 idle;
+// 4-7 expanders; 8-15 drain, two per 32-lane quarter, half the columns each.
+// The register file is re-split after launch (setmaxnreg): 64 per thread for
+// the first two warpgroups, 192 for the last two -- 512 threads x 128 at
+// launch.  Every mbarrier wait is bounded (tc_common.cuh).
+#include "gs_internal.cuh"
+#include "tc_common.cuh"
+
+namespace lowbit {
+namespace gsg {
+
+using namespace tc;
+
+constexpr int kRows = 128;                   // weight rows per CTA (the pair's MMA has M = 256)
+constexpr int BK = 128;                      // codes per stage
+constexpr int P_BYTES = kRows * BK / 2;      // packed tile of a stage
+constexpr int E_BYTES = kRows * BK;          // expanded tile
+constexpr int kExpStages = 2;
+constexpr int kThreads = 512;
+constexpr int kDrainWarps = 8;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kLaunchRegs = 128, kLeanRegs = 64, kDrainRegs = 192;
+static_assert(256 * kLeanRegs + 256 * kDrainRegs <= kThreads * kLaunchRegs, "the split must fit the launch");
+
+template <int NT> __host__ __device__ constexpr int q_bytes() { return NT / 2 * BK; }
+template <int NT> __host__ __device__ constexpr int stages() { return NT == 256 ? 7 : 8; }
+
+// The tiles of a call: token tiles expert after expert, each swept over the
+// weight rows (fastest), so that a round of pairs shares few token tiles and
+// an expert's weights are read together.
+struct Plan {
+    int32_t lo[LOWBIT_MOE_MAX_EXPERTS];         // an expert's token rows [lo, hi)
+    int32_t hi[LOWBIT_MOE_MAX_EXPERTS];
+    int32_t start[LOWBIT_MOE_MAX_EXPERTS + 1];  // its first token tile
+};
+
+template <int NT>
+__host__ __device__ constexpr size_t smem_bytes()
+{
+    return 1024 + static_cast<size_t>(stages<NT>()) * (q_bytes<NT>() + P_BYTES) +
+           static_cast<size_t>(kExpStages) * E_BYTES + kDrainWarps * NT / 2 * sizeof(float) + sizeof(Plan) + 16 +
+           8 * (2 * stages<NT>() + kExpStages + 8);
+}
+
+struct Tile {
+    int e;          // expert
+    int64_t row0;   // first token row
+    int64_t hi;     // end of the expert's rows
+    int64_t w0;     // first weight row of the pair
+};
+
+template <int NT>
+struct Tiles {
+    const Plan *plan;
+    int64_t next_id, step, total, num_w;
+    int e = 0;
+
+    __device__ Tiles(const Plan *p, int E, int64_t N) : plan(p)
+    {
+        next_id = blockIdx.x >> 1;
+        step = gridDim.x >> 1;
+        num_w = (N + 2 * kRows - 1) / (2 * kRows);
+        total = static_cast<int64_t>(p->start[E]) * num_w;
+    }
+    __device__ bool next(Tile &t)
+    {
+        if (next_id >= total) return false;
+        const int64_t tt = next_id / num_w;
+        while (tt >= plan->start[e + 1]) ++e;
+        t.e = e;
+        t.row0 = plan->lo[e] + (tt - plan->start[e]) * NT;
+        t.hi = plan->hi[e];
+        t.w0 = (next_id % num_w) * (2 * kRows);
+        next_id += step;
+        return true;
+    }
+};
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, uint64_t *bar, int x, int y, int z)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], [%2];"
+        ::"r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Arrive on both CTAs' barrier when the MMAs issued so far are complete.
+__device__ __forceinline__ void commit_both(uint64_t *bar)
+{
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+        ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(0x3)) : "memory");
+}
+
+__device__ __forceinline__ void commit_self(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+                 ::"r"(smem_u32(bar)) : "memory");
+}
+
+// s32 accumulate, s8 x s8, both K-major, M = 256, N = NT.
+template <int NT>
+__host__ __device__ constexpr uint32_t idesc()
+{
+    return (2u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(NT >> 3) << 17) |
+           (static_cast<uint32_t>((2 * kRows) >> 4) << 24);
+}
+
+// The 128 packed rows of a stage into the K-major 128B-swizzled int8 tile:
+// 16 packed bytes (32 codes) per thread and step; loads cover contiguous
+// bytes and the stores of 8 lanes hit 8 bank groups.
+__device__ __forceinline__ void expand(uint32_t P, uint32_t E, int et)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int i = et + 128 * j;
+        const int r = i >> 2, qd = i & 3;
+        const uint4 w = lds128(P + r * 64 + qd * 16);
+        const uint32_t row = E + r * 128;
+        sts128(row + (((2 * qd) ^ (r & 7)) << 4),
+               make_uint4(i4_expand(w.x, 0), i4_expand(w.x, 1), i4_expand(w.y, 0), i4_expand(w.y, 1)));
+        sts128(row + (((2 * qd + 1) ^ (r & 7)) << 4),
+               make_uint4(i4_expand(w.z, 0), i4_expand(w.z, 1), i4_expand(w.w, 0), i4_expand(w.w, 1)));
+    }
+}
+
+// acc += s * v for two elements in one instruction (each rounded as fmaf).
+__device__ __forceinline__ void fma2(float2 &acc, float s, float v0, float v1)
+{
+    asm("{\n\t.reg .b64 a, v, c;\n\t"
+        "mov.b64 a, {%2, %2};\n\tmov.b64 v, {%3, %4};\n\tmov.b64 c, {%0, %1};\n\t"
+        "fma.rn.f32x2 c, a, v, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y) : "f"(s), "f"(v0), "f"(v1));
+}
+
+template <int NT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_p, const GsArgs a)
+{
+    constexpr int ST = stages<NT>(), SE = kExpStages;
+    constexpr int Q_BYTES = q_bytes<NT>();
+    constexpr int NC = NT / 2;  // columns per drain warp
+    static_assert(SE < ST, "an expansion stage is freed through the MMA barrier of an older TMA stage");
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sQ = base;                          // ST token tiles, 1024-aligned
+    uint8_t *sE = sQ + ST * Q_BYTES;             // SE expanded tiles, 1024-aligned
+    uint8_t *sP = sE + SE * E_BYTES;             // ST packed tiles
+    float *sX = reinterpret_cast<float *>(sP + ST * P_BYTES);  // token scales, one copy per drain warp
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sX + kDrainWarps * NC);
+    uint64_t *full_tma = bars;                   // a stage's tiles have landed
+    uint64_t *mma_done = bars + ST;              // the MMAs that read the stage are complete
+    uint64_t *full_exp = bars + 2 * ST;          // both CTAs have expanded the stage (even CTA's is used)
+    uint64_t *acc_full = full_exp + SE;          // a group's sum is in accumulator b
+    uint64_t *acc_empty = acc_full + 2;          // both CTAs have drained it (even CTA's is used)
+    uint64_t *drain = acc_full + 4;
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(acc_full + 5);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(acc_full + 6);
+    Plan *plan = reinterpret_cast<Plan *>(acc_full + 7);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&full_tma[s], 1);
+            mbar_init(&mma_done[s], 1);
+        }
+        for (int s = 0; s < SE; ++s) mbar_init(&full_exp[s], 8);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&acc_full[b], 1);
+            mbar_init(&acc_empty[b], 2 * kDrainWarps);
+        }
+        mbar_init(drain, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_p)) : "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(smem_u32(const_cast<uint32_t *>(tmem_slot))), "r"(kTmemCols) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // both CTAs' barriers exist before any remote arrive
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+
+    // token tiles per expert, then their running sum
+    for (int e = threadIdx.x; e < a.E; e += kThreads) {
+        int64_t lo = 0, hi = a.M;
+        if (a.offsets != nullptr) gs_expert_rows(a.offsets, e, a.M, lo, hi, blockIdx.x == 0 ? a.status : nullptr);
+        plan->lo[e] = static_cast<int32_t>(lo);
+        plan->hi[e] = static_cast<int32_t>(hi);
+        plan->start[e + 1] = static_cast<int32_t>((hi - lo + NT - 1) / NT);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        int32_t run = 0;
+        for (int e0 = 0; e0 < a.E; e0 += 32) {
+            int32_t v = e0 + lane < a.E ? plan->start[e0 + lane + 1] : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t u = __shfl_up_sync(0xffffffffu, v, o);
+                if (lane >= o) v += u;
+            }
+            if (e0 + lane < a.E) plan->start[e0 + lane + 1] = run + v;
+            run += __shfl_sync(0xffffffffu, v, 31);
+        }
+        if (lane == 0) plan->start[0] = 0;
+    }
+    __syncthreads();
+
+    const int nkb = static_cast<int>((a.K + BK - 1) / BK);
+    const int nmma = static_cast<int>((a.K + UMMA_K - 1) / UMMA_K);  // per tile
+    const int per = 1 << (a.gshift - 5);                             // per group
+    const int groups = (nmma + per - 1) / per;
+    Tiles<NT> tiles(plan, a.E, a.N);
+    Tile tl;
+
+    if (warp < 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
+        if (warp == 0) {
+            // ---------------- TMA producer (both CTAs) ----------------
+            if (lane == 0) {
+                uint32_t g = 0;
+                bool ok = true;
+                while (ok && tiles.next(tl)) {
+                    const int t0 = static_cast<int>(tl.row0) + static_cast<int>(rank) * NC;
+                    const int w0 = static_cast<int>(tl.w0) + static_cast<int>(rank) * kRows;
+                    for (int kb = 0; kb < nkb; ++kb, ++g) {
+                        const int s = g % ST;
+                        if (!wait_bar(&mma_done[s], ((g / ST) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
+                        mbar_arrive_expect_tx(&full_tma[s], Q_BYTES + P_BYTES);
+                        tma_load_2d(sQ + s * Q_BYTES, &map_q, &full_tma[s], kb * BK, t0);
+                        tma_load_3d(sP + s * P_BYTES, &map_p, &full_tma[s], kb * (BK / 2), w0, tl.e);
+                    }
+                }
+                if (!ok) {
+                    for (uint32_t i = 0; i < ST && i < g; ++i) {
+                        const uint32_t gi = g - 1 - i;
+                        drain_bar(&full_tma[gi % ST], (gi / ST) & 1u);
+                    }
+                }
+            }
+        } else if (warp == 1) {
+            // ---------------- MMA issuer (even CTA) ----------------
+            if (leader && lane == 0) {
+                const uint64_t qdesc0 = sw128_desc(smem_u32(sQ)), edesc0 = sw128_desc(smem_u32(sE));
+                uint32_t g = 0, h = 0;  // K blocks and groups so far
+                bool ok = true;
+                while (ok && tiles.next(tl)) {
+                    int m = 0;
+                    for (int kb = 0; ok && kb < nkb; ++kb, ++g) {
+                        const int s1 = g % ST, s2 = g % SE;
+                        if (!wait_bar(&full_exp[s2], (g / SE) & 1u, abort_flag, a.status)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint64_t qdesc = qdesc0 + static_cast<uint64_t>((s1 * Q_BYTES) >> 4);
+                        const uint64_t edesc = edesc0 + static_cast<uint64_t>((s2 * E_BYTES) >> 4);
+                        for (int kk = 0; kk < BK / UMMA_K && m < nmma; ++kk, ++m) {
+                            const int b = h & 1;
+                            const bool first = (m & (per - 1)) == 0;
+                            if (first) {
+                                if (!wait_bar(&acc_empty[b], ((h >> 1) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
+                                tc_fence_after();
+                            }
+                            mma_i8_pair(tmem_base + static_cast<uint32_t>(b * NT),
+                                        edesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)),
+                                        qdesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)), idesc<NT>(), first ? 0u : 1u);
+                            if (((m + 1) & (per - 1)) == 0 || m + 1 == nmma) {
+                                commit_both(&acc_full[b]);
+                                ++h;
+                            }
+                        }
+                        if (ok) commit_both(&mma_done[s1]);
+                    }
+                }
+                commit_self(drain);
+                drain_bar(drain, 0);
+            }
+        } else if (warp >= 4) {
+            // ---------------- expanders: own 128 weight rows ----------------
+            const int et = threadIdx.x - 128;
+            const uint32_t p_base = smem_u32(sP), e_base = smem_u32(sE);
+            const uint32_t full_exp_leader = map_to_peer(smem_u32(full_exp), 0);
+            uint32_t g = 0;
+            bool ok = true;
+            while (ok && tiles.next(tl)) {
+                for (int kb = 0; kb < nkb; ++kb, ++g) {
+                    const int s1 = g % ST, s2 = g % SE;
+                    if (!wait_bar(&full_tma[s1], (g / ST) & 1u, abort_flag, a.status)) { ok = false; break; }
+                    if (g >= static_cast<uint32_t>(SE)) {
+                        const uint32_t gp = g - SE;
+                        if (!wait_bar(&mma_done[gp % ST], (gp / ST) & 1u, abort_flag, a.status)) { ok = false; break; }
+                    }
+                    expand(p_base + s1 * P_BYTES, e_base + s2 * E_BYTES, et);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_remote(full_exp_leader + static_cast<uint32_t>(s2 * 8));
+                }
+            }
+        }
+    } else {
+        // ---------------- drain: own 128 weight rows x NT tokens ----------------
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
+        const int quarter = warp & 3, half = (warp - 8) >> 2;
+        float *sx = sX + (warp - 8) * NC;
+        const uint32_t acc_empty_leader = map_to_peer(smem_u32(acc_empty), 0);
+        const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * NC);
+        uint32_t h = 0;
+        bool ok = true;
+        while (ok && tiles.next(tl)) {
+            const int64_t n = tl.w0 + rank * kRows + quarter * 32 + lane;
+            const bool row_on = n < a.N;
+            const int64_t s_at = tl.e * a.sstride + n * a.lds;
+            const int64_t row0 = tl.row0 + half * NC;  // this warp's first token
+            const int64_t left = tl.hi - row0;
+            // the factor 16 of the shifted codes leaves with the token scale
+#pragma unroll
+            for (int i = lane; i < NC; i += 32) sx[i] = i < left ? __fmul_rn(ld_act_f32(a.s_x + row0 + i), 0.0625f) : 0.0f;
+            __syncwarp();
+            float2 acc[NC / 2];
+#pragma unroll
+            for (int j = 0; j < NC / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+            float s_next = row_on ? gs_scale(a.s_g, s_at, a.s_bf16) : 0.0f;
+            for (int gr = 0; gr < groups; ++gr, ++h) {
+                const int b = h & 1;
+                const float s = s_next;
+                if (gr + 1 < groups && row_on) s_next = gs_scale(a.s_g, s_at + gr + 1, a.s_bf16);
+                int ready = 0;
+                if (lane == 0) ready = wait_bar(&acc_full[b], (h >> 1) & 1u, abort_flag, a.status) ? 1 : 0;
+                ready = __shfl_sync(0xffffffffu, ready, 0);
+                if (!ready) { ok = false; break; }
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < NC / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_32cols(tacc + static_cast<uint32_t>(b * NT + c * 32), v);
+                    if (c == NC / 32 - 1) {
+                        // the buffer is in registers: the next group may use it
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(acc_empty_leader + static_cast<uint32_t>(b * 8));
+                    }
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        fma2(acc[16 * c + j], s, __int2float_rn(static_cast<int32_t>(v[2 * j])),
+                             __int2float_rn(static_cast<int32_t>(v[2 * j + 1])));
+                }
+            }
+            if (ok && row_on) {
+                const uint32_t sx_at = smem_u32(sx);
+#pragma unroll
+                for (int j = 0; j < NC; j += 4) {
+                    const uint4 x4 = lds128(sx_at + j * 4);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 p = acc[(j + i) / 2];
+                        const float f = __fmul_rn(i & 1 ? p.y : p.x, __uint_as_float((&x4.x)[i]));
+                        if (j + i < left) {
+                            const int64_t at = (row0 + j + i) * a.ldy + n;
+                            if (a.y_bf16) static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(f);
+                            else static_cast<float *>(a.y)[at] = f;
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        }
+    }
+
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the pair's MMAs and remote arrivals are over
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
+                     : "memory");
+    }
+}
+
+// Pairs that can be resident at once, found (with the shared-memory attribute
+// set) on the first launch on each device.
+template <int NT>
+int resident_pairs(int dev)
+{
+    constexpr size_t smem = smem_bytes<NT>();
+    static_assert(smem <= 232448, "shared memory budget");
+    static PerDevice pairs;
+    return pairs.get(dev, [&] {
+        if (cudaFuncSetAttribute(gs_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 static_cast<int>(smem)) != cudaSuccess)
+            return 0;
+        // the register split needs all of the launch's registers
+        cudaFuncAttributes at;
+        if (cudaFuncGetAttributes(&at, gs_gemm_kernel<NT>) != cudaSuccess || at.numRegs < kLaunchRegs) return 0;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(2 * static_cast<unsigned>(device_sm_count() / 2));
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = smem;
+        int n = 0;
+        return cudaOccupancyMaxActiveClusters(&n, gs_gemm_kernel<NT>, &cfg) == cudaSuccess ? n : 0;
+    });
+}
+
+// Packed weights [E][N][ldp] as a 3-D map; boxes of one stage's 64 bytes x 128 rows.
+bool make_weight_map(CUtensorMap *map, const GsArgs &a)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(4 * ((a.K + 7) / 8)), static_cast<cuuint64_t>(a.N),
+                                static_cast<cuuint64_t>(a.E)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(a.ldp),
+                                   static_cast<cuuint64_t>(a.E > 1 ? a.pstride : a.N * a.ldp)};
+    const cuuint32_t box[3] = {BK / 2, kRows, 1};
+    const cuuint32_t estride[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<uint8_t *>(a.packed), dims, strides, box, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int NT>
+lowbit_status launch(const GsArgs &a, cudaStream_t st)
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
+    const int64_t resident = resident_pairs<NT>(dev);
+    if (resident <= 0) return LOWBIT_ERR_CUDA;
+    CUtensorMap mq, mp;
+    if (!make_map_2d(&mq, a.q, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M), static_cast<uint64_t>(a.ldq), BK,
+                     NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_weight_map(&mp, a))
+        return LOWBIT_ERR_CUDA;
+    // experts: their row counts are on the device; at most this many token tiles
+    const int64_t token_tiles = a.M / NT + (a.offsets != nullptr ? a.E : 1);
+    int64_t pairs = token_tiles * ((a.N + 2 * kRows - 1) / (2 * kRows));
+    if (pairs > resident) pairs = resident;
+    return launch_pdl(gs_gemm_kernel<NT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem_bytes<NT>(), st,
+                      0, mq, mp, a);
+}
+
+}  // namespace gsg
+
+lowbit_status set_wait_limit_gs(long long cycles) { return tc::set_wait_limit_here(cycles); }
+
+lowbit_status gs_gemm_launch(const GsArgs &a, cudaStream_t st)
+{
+    const int64_t rows = a.offsets != nullptr ? a.M / a.E : a.M;
+    if (rows > 128) return gsg::launch<256>(a, st);
+    if (rows > 64) return gsg::launch<128>(a, st);
+    return gsg::launch<64>(a, st);
+}
+
+}  // namespace lowbit

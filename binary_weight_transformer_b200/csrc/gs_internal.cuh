@@ -61,6 +61,7 @@ __device__ __forceinline__ void gs_expert_rows(const int32_t *offsets, int e, in
 }
 
 lowbit_status gs_mma_launch(const GsArgs &a, cudaStream_t st);
+lowbit_status gs_gemm_launch(const GsArgs &a, cudaStream_t st);
 lowbit_status gs_pack_launch(const void *w, int w_bf16, int64_t N, int64_t K, int64_t ldw, int gshift, uint8_t *packed,
                              int64_t ldp, void *s_g, int s_bf16, int64_t lds, int32_t *status, cudaStream_t st);
 lowbit_status gs_unpack_launch(const uint8_t *packed, int64_t ldp, const void *s_g, int s_bf16, int64_t lds, int64_t N,
