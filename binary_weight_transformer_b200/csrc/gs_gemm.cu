@@ -64,35 +64,37 @@ __host__ __device__ constexpr size_t smem_bytes()
 }
 
 struct Tile {
-    int e;          // expert
-    int64_t row0;   // first token row
-    int64_t hi;     // end of the expert's rows
-    int64_t w0;     // first weight row of the pair
+    int e;     // expert
+    int row0;  // first token row
+    int hi;    // end of the expert's rows
+    int w0;    // first weight row of the pair
 };
 
+// Tile ids fit 32 bits: a tile is at least 256 x 64 outputs.  Each role makes
+// its own iterator, after the register split: one made before it stays in
+// registers that the drain needs, and its spill slowed the MMA thread's loop.
 template <int NT>
 struct Tiles {
     const Plan *plan;
-    int64_t next_id, step, total, num_w;
+    uint32_t id, total, num_w;
     int e = 0;
 
-    __device__ Tiles(const Plan *p, int E, int64_t N) : plan(p)
+    __device__ __forceinline__ Tiles(const Plan *p, int E, int64_t N) : plan(p)
     {
-        next_id = blockIdx.x >> 1;
-        step = gridDim.x >> 1;
-        num_w = (N + 2 * kRows - 1) / (2 * kRows);
-        total = static_cast<int64_t>(p->start[E]) * num_w;
+        id = blockIdx.x >> 1;
+        num_w = static_cast<uint32_t>((N + 2 * kRows - 1) / (2 * kRows));
+        total = static_cast<uint32_t>(p->start[E]) * num_w;
     }
-    __device__ bool next(Tile &t)
+    __device__ __forceinline__ bool next(Tile &t)
     {
-        if (next_id >= total) return false;
-        const int64_t tt = next_id / num_w;
+        if (id >= total) return false;
+        const int tt = static_cast<int>(id / num_w);
         while (tt >= plan->start[e + 1]) ++e;
         t.e = e;
         t.row0 = plan->lo[e] + (tt - plan->start[e]) * NT;
         t.hi = plan->hi[e];
-        t.w0 = (next_id % num_w) * (2 * kRows);
-        next_id += step;
+        t.w0 = static_cast<int>(id % num_w) * (2 * kRows);
+        id += gridDim.x >> 1;
         return true;
     }
 };
@@ -156,22 +158,64 @@ __device__ __forceinline__ void expand(uint32_t P, uint32_t E, int et)
     }
 }
 
-// acc += s * v for two elements in one instruction (each rounded as fmaf).
-__device__ __forceinline__ void fma2(float2 &acc, float s, float v0, float v1)
+// acc += s * float(v) for two elements.  A sum (at most 256 codes of 16 * 7
+// times 128, below 2^22) becomes a float by bits: its low 23 bits with bit 22
+// (a copy of the sign) turned over, under the exponent of 2^23, are the float
+// 1.5 * 2^23 + v.  That is one logic instruction, on a pipe that the
+// multiply-adds do not use (an integer addition is compiled onto theirs, and
+// the conversion instruction's pipe is narrower still); the subtraction of
+// 1.5 * 2^23, which is exact, and the multiply-add take two elements each.
+__device__ __forceinline__ float biased(uint32_t v)
 {
-    asm("{\n\t.reg .b64 a, v, c;\n\t"
-        "mov.b64 a, {%2, %2};\n\tmov.b64 v, {%3, %4};\n\tmov.b64 c, {%0, %1};\n\t"
-        "fma.rn.f32x2 c, a, v, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
-        : "+f"(acc.x), "+f"(acc.y) : "f"(s), "f"(v0), "f"(v1));
+    uint32_t r;
+    asm("lop3.b32 %0, %1, 0x007FFFFF, 0x4B400000, 0x6A;" : "=r"(r) : "r"(v));  // (v & mask) ^ bits
+    return __uint_as_float(r);
 }
 
-template <int NT>
+__device__ __forceinline__ void fma2(float2 &acc, float s, uint32_t v0, uint32_t v1)
+{
+    asm("{\n\t.reg .b64 a, v, c, m;\n\t"
+        "mov.b64 a, {%2, %2};\n\tmov.b64 v, {%3, %4};\n\tmov.b64 c, {%0, %1};\n\tmov.b64 m, {%5, %5};\n\t"
+        "add.rn.f32x2 v, v, m;\n\t"
+        "fma.rn.f32x2 c, a, v, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
+        : "+f"(acc.x), "+f"(acc.y)
+        : "f"(s), "f"(biased(v0)), "f"(biased(v1)), "f"(-12582912.0f));
+}
+
+__device__ __forceinline__ void store_as(__nv_bfloat16 *p, float f) { *p = __float2bfloat16_rn(f); }
+__device__ __forceinline__ void store_as(float *p, float f) { *p = f; }
+
+// The thread's weight row n of tokens row0 .. row0 + min(left, NC) - 1: the
+// 32 lanes of a warp hold consecutive n, so a store covers 64 (bf16) or 128
+// consecutive bytes.
+template <typename T, int NC>
+__device__ __forceinline__ void store_columns(void *y, int64_t ldy, int row0, int n, int left, uint32_t sx,
+                                              const float2 (&acc)[NC / 2])
+{
+    T *p = static_cast<T *>(y) + row0 * ldy + n;
+#pragma unroll
+    for (int j = 0; j < NC; j += 4) {
+        const uint4 x = lds128(sx + j * 4);
+        const float f[4] = {__fmul_rn(acc[j / 2].x, __uint_as_float(x.x)), __fmul_rn(acc[j / 2].y, __uint_as_float(x.y)),
+                            __fmul_rn(acc[j / 2 + 1].x, __uint_as_float(x.z)),
+                            __fmul_rn(acc[j / 2 + 1].y, __uint_as_float(x.w))};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (j + i < left) store_as(p, f[i]);
+            p += ldy;
+        }
+    }
+}
+
+// NT tokens per tile; PER MMAs of 32 codes per group (group / 32).
+template <int NT, int PER>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_p, const GsArgs a)
 {
     constexpr int ST = stages<NT>(), SE = kExpStages;
     constexpr int Q_BYTES = q_bytes<NT>();
-    constexpr int NC = NT / 2;  // columns per drain warp
+    constexpr int NC = NT / 2;                   // columns per drain warp
+    constexpr int FPB = PER >= 4 ? 1 : 4 / PER;  // groups that end in a K block (PER = 8: in every other one)
     static_assert(SE < ST, "an expansion stage is freed through the MMA barrier of an older TMA stage");
 
     extern __shared__ uint8_t smem_raw[];
@@ -182,9 +226,9 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     float *sX = reinterpret_cast<float *>(sP + ST * P_BYTES);  // token scales, one copy per drain warp
     uint64_t *bars = reinterpret_cast<uint64_t *>(sX + kDrainWarps * NC);
     uint64_t *full_tma = bars;                   // a stage's tiles have landed
-    uint64_t *mma_done = bars + ST;              // the MMAs that read the stage are complete
+    uint64_t *mma_done = bars + ST;              // the stage's MMAs, and its last group, are complete
     uint64_t *full_exp = bars + 2 * ST;          // both CTAs have expanded the stage (even CTA's is used)
-    uint64_t *acc_full = full_exp + SE;          // a group's sum is in accumulator b
+    uint64_t *acc_full = full_exp + SE;          // a group that is not the stage's last is in accumulator b
     uint64_t *acc_empty = acc_full + 2;          // both CTAs have drained it (even CTA's is used)
     uint64_t *drain = acc_full + 4;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(acc_full + 5);
@@ -250,22 +294,18 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     __syncthreads();
 
     const int nkb = static_cast<int>((a.K + BK - 1) / BK);
-    const int nmma = static_cast<int>((a.K + UMMA_K - 1) / UMMA_K);  // per tile
-    const int per = 1 << (a.gshift - 5);                             // per group
-    const int groups = (nmma + per - 1) / per;
-    Tiles<NT> tiles(plan, a.E, a.N);
-    Tile tl;
-
     if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
         if (warp == 0) {
             // ---------------- TMA producer (both CTAs) ----------------
             if (lane == 0) {
+                Tiles<NT> tiles(plan, a.E, a.N);
+                Tile tl;
                 uint32_t g = 0;
                 bool ok = true;
                 while (ok && tiles.next(tl)) {
-                    const int t0 = static_cast<int>(tl.row0) + static_cast<int>(rank) * NC;
-                    const int w0 = static_cast<int>(tl.w0) + static_cast<int>(rank) * kRows;
+                    const int t0 = tl.row0 + static_cast<int>(rank) * NC;
+                    const int w0 = tl.w0 + static_cast<int>(rank) * kRows;
                     for (int kb = 0; kb < nkb; ++kb, ++g) {
                         const int s = g % ST;
                         if (!wait_bar(&mma_done[s], ((g / ST) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
@@ -285,30 +325,34 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             // ---------------- MMA issuer (even CTA) ----------------
             if (leader && lane == 0) {
                 const uint64_t qdesc0 = sw128_desc(smem_u32(sQ)), edesc0 = sw128_desc(smem_u32(sE));
+                Tiles<NT> tiles(plan, a.E, a.N);
+                Tile tl;
                 uint32_t g = 0, h = 0;  // K blocks and groups so far
                 bool ok = true;
+                // Straight code between the waits: with the group's end
+                // decided MMA by MMA in a loop, the same work took twice as
+                // long to issue.  K blocks are whole: past K the token codes
+                // are zero.
                 while (ok && tiles.next(tl)) {
-                    int m = 0;
                     for (int kb = 0; ok && kb < nkb; ++kb, ++g) {
                         const int s1 = g % ST, s2 = g % SE;
-                        if (!wait_bar(&full_exp[s2], (g / SE) & 1u, abort_flag, a.status)) { ok = false; break; }
-                        tc_fence_after();
                         const uint64_t qdesc = qdesc0 + static_cast<uint64_t>((s1 * Q_BYTES) >> 4);
                         const uint64_t edesc = edesc0 + static_cast<uint64_t>((s2 * E_BYTES) >> 4);
-                        for (int kk = 0; kk < BK / UMMA_K && m < nmma; ++kk, ++m) {
+                        const bool opens = PER <= 4 || (kb & 1) == 0;
+#pragma unroll
+                        for (int f = 0; f < FPB; ++f) {
                             const int b = h & 1;
-                            const bool first = (m & (per - 1)) == 0;
-                            if (first) {
-                                if (!wait_bar(&acc_empty[b], ((h >> 1) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
-                                tc_fence_after();
-                            }
-                            mma_i8_pair(tmem_base + static_cast<uint32_t>(b * NT),
-                                        edesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)),
-                                        qdesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)), idesc<NT>(), first ? 0u : 1u);
-                            if (((m + 1) & (per - 1)) == 0 || m + 1 == nmma) {
-                                commit_both(&acc_full[b]);
-                                ++h;
-                            }
+                            if (opens && !wait_bar(&acc_empty[b], ((h >> 1) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
+                            if (f == 0 && !wait_bar(&full_exp[s2], (g / SE) & 1u, abort_flag, a.status)) { ok = false; break; }
+                            tc_fence_after();
+                            const uint32_t d = tmem_base + static_cast<uint32_t>(b * NT);
+#pragma unroll
+                            for (int kk = f * 4 / FPB; kk < (f + 1) * 4 / FPB; ++kk)
+                                mma_i8_pair(d, edesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)),
+                                            qdesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)), idesc<NT>(),
+                                            kk == f * 4 / FPB && opens ? 0u : 1u);
+                            if (f + 1 < FPB) commit_both(&acc_full[b]);
+                            if (PER <= 4 || (kb & 1) != 0 || kb + 1 == nkb) ++h;
                         }
                         if (ok) commit_both(&mma_done[s1]);
                     }
@@ -321,6 +365,8 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const int et = threadIdx.x - 128;
             const uint32_t p_base = smem_u32(sP), e_base = smem_u32(sE);
             const uint32_t full_exp_leader = map_to_peer(smem_u32(full_exp), 0);
+            Tiles<NT> tiles(plan, a.E, a.N);
+            Tile tl;
             uint32_t g = 0;
             bool ok = true;
             while (ok && tiles.next(tl)) {
@@ -345,14 +391,17 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         float *sx = sX + (warp - 8) * NC;
         const uint32_t acc_empty_leader = map_to_peer(smem_u32(acc_empty), 0);
         const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * NC);
-        uint32_t h = 0;
+        Tiles<NT> tiles(plan, a.E, a.N);
+        Tile tl;
+        const int groups = static_cast<int>((a.K - 1) >> a.gshift) + 1;
+        uint32_t g = 0, h = 0, full0 = 0, full1 = 0;  // K blocks, groups, and completions of acc_full so far
         bool ok = true;
         while (ok && tiles.next(tl)) {
-            const int64_t n = tl.w0 + rank * kRows + quarter * 32 + lane;
+            const int n = tl.w0 + static_cast<int>(rank) * kRows + quarter * 32 + lane;
             const bool row_on = n < a.N;
-            const int64_t s_at = tl.e * a.sstride + n * a.lds;
-            const int64_t row0 = tl.row0 + half * NC;  // this warp's first token
-            const int64_t left = tl.hi - row0;
+            const int64_t s_at = tl.e * a.sstride + static_cast<int64_t>(n) * a.lds;
+            const int row0 = tl.row0 + half * NC;  // this warp's first token
+            const int left = tl.hi - row0;
             // the factor 16 of the shifted codes leaves with the token scale
 #pragma unroll
             for (int i = lane; i < NC; i += 32) sx[i] = i < left ? __fmul_rn(ld_act_f32(a.s_x + row0 + i), 0.0625f) : 0.0f;
@@ -361,47 +410,40 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
             for (int j = 0; j < NC / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
             float s_next = row_on ? gs_scale(a.s_g, s_at, a.s_bf16) : 0.0f;
-            for (int gr = 0; gr < groups; ++gr, ++h) {
-                const int b = h & 1;
-                const float s = s_next;
-                if (gr + 1 < groups && row_on) s_next = gs_scale(a.s_g, s_at + gr + 1, a.s_bf16);
-                int ready = 0;
-                if (lane == 0) ready = wait_bar(&acc_full[b], (h >> 1) & 1u, abort_flag, a.status) ? 1 : 0;
-                ready = __shfl_sync(0xffffffffu, ready, 0);
-                if (!ready) { ok = false; break; }
-                tc_fence_after();
+            int gr = 0;  // group of the row
+            for (int kb = 0; ok && kb < nkb; ++kb, ++g) {
+                if (PER == 8 && (kb & 1) == 0 && kb + 1 < nkb) continue;  // the group goes on
 #pragma unroll
-                for (int c = 0; c < NC / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32cols(tacc + static_cast<uint32_t>(b * NT + c * 32), v);
-                    if (c == NC / 32 - 1) {
-                        // the buffer is in registers: the next group may use it
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_remote(acc_empty_leader + static_cast<uint32_t>(b * 8));
+                for (int f = 0; f < FPB; ++f, ++gr) {
+                    const int b = h & 1;
+                    const float s = s_next;
+                    s_next = gr + 1 < groups && row_on ? gs_scale(a.s_g, s_at + gr + 1, a.s_bf16) : 0.0f;
+                    uint64_t *full = f + 1 == FPB ? &mma_done[g % ST] : &acc_full[b];
+                    const uint32_t phase = f + 1 == FPB ? g / ST : b == 0 ? full0++ : full1++;
+                    ++h;
+                    int ready = 0;
+                    if (lane == 0) ready = wait_bar(full, phase & 1u, abort_flag, a.status) ? 1 : 0;
+                    ready = __shfl_sync(0xffffffffu, ready, 0);
+                    if (!ready) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < NC / 32; ++c) {
+                        uint32_t v[32];
+                        tmem_ld_32cols(tacc + static_cast<uint32_t>(b * NT + c * 32), v);
+                        if (c == NC / 32 - 1) {
+                            // the buffer is in registers: the next group may use it
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_remote(acc_empty_leader + static_cast<uint32_t>(b * 8));
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], s, v[2 * j], v[2 * j + 1]);
                     }
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        fma2(acc[16 * c + j], s, __int2float_rn(static_cast<int32_t>(v[2 * j])),
-                             __int2float_rn(static_cast<int32_t>(v[2 * j + 1])));
                 }
             }
             if (ok && row_on) {
-                const uint32_t sx_at = smem_u32(sx);
-#pragma unroll
-                for (int j = 0; j < NC; j += 4) {
-                    const uint4 x4 = lds128(sx_at + j * 4);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 p = acc[(j + i) / 2];
-                        const float f = __fmul_rn(i & 1 ? p.y : p.x, __uint_as_float((&x4.x)[i]));
-                        if (j + i < left) {
-                            const int64_t at = (row0 + j + i) * a.ldy + n;
-                            if (a.y_bf16) static_cast<__nv_bfloat16 *>(a.y)[at] = __float2bfloat16_rn(f);
-                            else static_cast<float *>(a.y)[at] = f;
-                        }
-                    }
-                }
+                if (a.y_bf16) store_columns<__nv_bfloat16, NC>(a.y, a.ldy, row0, n, left, smem_u32(sx), acc);
+                else store_columns<float, NC>(a.y, a.ldy, row0, n, left, smem_u32(sx), acc);
             }
             __syncwarp();
         }
@@ -420,25 +462,25 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 
 // Pairs that can be resident at once, found (with the shared-memory attribute
 // set) on the first launch on each device.
-template <int NT>
+template <int NT, int PER>
 int resident_pairs(int dev)
 {
     constexpr size_t smem = smem_bytes<NT>();
     static_assert(smem <= 232448, "shared memory budget");
     static PerDevice pairs;
     return pairs.get(dev, [&] {
-        if (cudaFuncSetAttribute(gs_gemm_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(gs_gemm_kernel<NT, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(smem)) != cudaSuccess)
             return 0;
         // the register split needs all of the launch's registers
         cudaFuncAttributes at;
-        if (cudaFuncGetAttributes(&at, gs_gemm_kernel<NT>) != cudaSuccess || at.numRegs < kLaunchRegs) return 0;
+        if (cudaFuncGetAttributes(&at, gs_gemm_kernel<NT, PER>) != cudaSuccess || at.numRegs < kLaunchRegs) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * static_cast<unsigned>(device_sm_count() / 2));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = smem;
         int n = 0;
-        return cudaOccupancyMaxActiveClusters(&n, gs_gemm_kernel<NT>, &cfg) == cudaSuccess ? n : 0;
+        return cudaOccupancyMaxActiveClusters(&n, gs_gemm_kernel<NT, PER>, &cfg) == cudaSuccess ? n : 0;
     });
 }
 
@@ -458,12 +500,12 @@ bool make_weight_map(CUtensorMap *map, const GsArgs &a)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT>
+template <int NT, int PER>
 lowbit_status launch(const GsArgs &a, cudaStream_t st)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
-    const int64_t resident = resident_pairs<NT>(dev);
+    const int64_t resident = resident_pairs<NT, PER>(dev);
     if (resident <= 0) return LOWBIT_ERR_CUDA;
     CUtensorMap mq, mp;
     if (!make_map_2d(&mq, a.q, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M), static_cast<uint64_t>(a.ldq), BK,
@@ -474,8 +516,19 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
     const int64_t token_tiles = a.M / NT + (a.offsets != nullptr ? a.E : 1);
     int64_t pairs = token_tiles * ((a.N + 2 * kRows - 1) / (2 * kRows));
     if (pairs > resident) pairs = resident;
-    return launch_pdl(gs_gemm_kernel<NT>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem_bytes<NT>(), st,
+    return launch_pdl(gs_gemm_kernel<NT, PER>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem_bytes<NT>(), st,
                       0, mq, mp, a);
+}
+
+template <int NT>
+lowbit_status launch_g(const GsArgs &a, cudaStream_t st)
+{
+    switch (a.gshift) {
+    case 5: return launch<NT, 1>(a, st);
+    case 6: return launch<NT, 2>(a, st);
+    case 7: return launch<NT, 4>(a, st);
+    default: return launch<NT, 8>(a, st);
+    }
 }
 
 }  // namespace gsg
@@ -485,9 +538,9 @@ lowbit_status set_wait_limit_gs(long long cycles) { return tc::set_wait_limit_he
 lowbit_status gs_gemm_launch(const GsArgs &a, cudaStream_t st)
 {
     const int64_t rows = a.offsets != nullptr ? a.M / a.E : a.M;
-    if (rows > 128) return gsg::launch<256>(a, st);
-    if (rows > 64) return gsg::launch<128>(a, st);
-    return gsg::launch<64>(a, st);
+    if (rows > 128) return gsg::launch_g<256>(a, st);
+    if (rows > 64) return gsg::launch_g<128>(a, st);
+    return gsg::launch_g<64>(a, st);
 }
 
 }  // namespace lowbit
