@@ -60,7 +60,7 @@ __host__ __device__ constexpr size_t smem_bytes()
 {
     return 1024 + static_cast<size_t>(stages<NT>()) * (q_bytes<NT>() + P_BYTES) +
            static_cast<size_t>(kExpStages) * E_BYTES + kDrainWarps * NT / 2 * sizeof(float) + sizeof(Plan) + 16 +
-           8 * (2 * stages<NT>() + kExpStages + 8);
+           8 * (2 * stages<NT>() + kExpStages + 12);
 }
 
 struct Tile {
@@ -158,28 +158,26 @@ __device__ __forceinline__ void expand(uint32_t P, uint32_t E, int et)
     }
 }
 
-// acc += s * float(v) for two elements.  A sum (at most 256 codes of 16 * 7
-// times 128, below 2^22) becomes a float by bits: its low 23 bits with bit 22
-// (a copy of the sign) turned over, under the exponent of 2^23, are the float
-// 1.5 * 2^23 + v.  That is one logic instruction, on a pipe that the
-// multiply-adds do not use (an integer addition is compiled onto theirs, and
-// the conversion instruction's pipe is narrower still); the subtraction of
-// 1.5 * 2^23, which is exact, and the multiply-add take two elements each.
-__device__ __forceinline__ float biased(uint32_t v)
-{
-    uint32_t r;
-    asm("lop3.b32 %0, %1, 0x007FFFFF, 0x4B400000, 0x6A;" : "=r"(r) : "r"(v));  // (v & mask) ^ bits
-    return __uint_as_float(r);
-}
+// The group scales of one weight row.
+template <bool SB>
+struct ScaleRow {
+    const void *row;
+    __device__ __forceinline__ ScaleRow(const void *s, int64_t at)
+        : row(SB ? static_cast<const void *>(static_cast<const uint16_t *>(s) + at)
+                 : static_cast<const void *>(static_cast<const float *>(s) + at))
+    {
+    }
+    __device__ __forceinline__ float at(int g) const { return gs_scale(row, g, SB); }
+};
 
+// acc += s * float(v) for two elements.
 __device__ __forceinline__ void fma2(float2 &acc, float s, uint32_t v0, uint32_t v1)
 {
-    asm("{\n\t.reg .b64 a, v, c, m;\n\t"
-        "mov.b64 a, {%2, %2};\n\tmov.b64 v, {%3, %4};\n\tmov.b64 c, {%0, %1};\n\tmov.b64 m, {%5, %5};\n\t"
-        "add.rn.f32x2 v, v, m;\n\t"
+    asm("{\n\t.reg .b64 a, v, c;\n\t"
+        "mov.b64 a, {%2, %2};\n\tmov.b64 v, {%3, %4};\n\tmov.b64 c, {%0, %1};\n\t"
         "fma.rn.f32x2 c, a, v, c;\n\tmov.b64 {%0, %1}, c;\n\t}"
         : "+f"(acc.x), "+f"(acc.y)
-        : "f"(s), "f"(biased(v0)), "f"(biased(v1)), "f"(-12582912.0f));
+        : "f"(s), "f"(__int2float_rn(static_cast<int>(v0))), "f"(__int2float_rn(static_cast<int>(v1))));
 }
 
 __device__ __forceinline__ void store_as(__nv_bfloat16 *p, float f) { *p = __float2bfloat16_rn(f); }
@@ -207,14 +205,15 @@ __device__ __forceinline__ void store_columns(void *y, int64_t ldy, int row0, in
     }
 }
 
-// NT tokens per tile; PER MMAs of 32 codes per group (group / 32).
-template <int NT, int PER>
+// NT tokens per tile; PER MMAs of 32 codes per group (group / 32); SB: bf16 scales.
+template <int NT, int PER, bool SB>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_p, const GsArgs a)
 {
     constexpr int ST = stages<NT>(), SE = kExpStages;
     constexpr int Q_BYTES = q_bytes<NT>();
-    constexpr int NC = NT / 2;                   // columns per drain warp
+    constexpr int SUB = NT / 2;                  // tokens of a half: of one MMA and of a drain warp
+    constexpr int QR = SUB / 2;                  // tokens of a half that each CTA stages
     constexpr int FPB = PER >= 4 ? 1 : 4 / PER;  // groups that end in a K block (PER = 8: in every other one)
     static_assert(SE < ST, "an expansion stage is freed through the MMA barrier of an older TMA stage");
 
@@ -224,16 +223,16 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     uint8_t *sE = sQ + ST * Q_BYTES;             // SE expanded tiles, 1024-aligned
     uint8_t *sP = sE + SE * E_BYTES;             // ST packed tiles
     float *sX = reinterpret_cast<float *>(sP + ST * P_BYTES);  // token scales, one copy per drain warp
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sX + kDrainWarps * NC);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sX + kDrainWarps * SUB);
     uint64_t *full_tma = bars;                   // a stage's tiles have landed
-    uint64_t *mma_done = bars + ST;              // the stage's MMAs, and its last group, are complete
+    uint64_t *mma_done = bars + ST;              // both halves' MMAs on the stage are complete
     uint64_t *full_exp = bars + 2 * ST;          // both CTAs have expanded the stage (even CTA's is used)
-    uint64_t *acc_full = full_exp + SE;          // a group that is not the stage's last is in accumulator b
-    uint64_t *acc_empty = acc_full + 2;          // both CTAs have drained it (even CTA's is used)
-    uint64_t *drain = acc_full + 4;
-    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(acc_full + 5);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(acc_full + 6);
-    Plan *plan = reinterpret_cast<Plan *>(acc_full + 7);
+    uint64_t *acc_full = full_exp + SE;          // [half][b]: a group's sums are in accumulator b of a half
+    uint64_t *acc_empty = acc_full + 4;          // [half][b]: both CTAs have drained it (even CTA's is used)
+    uint64_t *drain = acc_full + 8;              // [half]
+    volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(acc_full + 10);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(acc_full + 11);
+    Plan *plan = reinterpret_cast<Plan *>(acc_full + 12);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -242,14 +241,14 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(&full_tma[s], 1);
-            mbar_init(&mma_done[s], 1);
+            mbar_init(&mma_done[s], 2);
         }
         for (int s = 0; s < SE; ++s) mbar_init(&full_exp[s], 8);
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < 4; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], 2 * kDrainWarps);
+            mbar_init(&acc_empty[b], kDrainWarps);
         }
-        mbar_init(drain, 1);
+        for (int x = 0; x < 2; ++x) mbar_init(&drain[x], 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
@@ -304,13 +303,14 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 uint32_t g = 0;
                 bool ok = true;
                 while (ok && tiles.next(tl)) {
-                    const int t0 = tl.row0 + static_cast<int>(rank) * NC;
+                    const int t0 = tl.row0 + static_cast<int>(rank) * QR;
                     const int w0 = tl.w0 + static_cast<int>(rank) * kRows;
                     for (int kb = 0; kb < nkb; ++kb, ++g) {
                         const int s = g % ST;
                         if (!wait_bar(&mma_done[s], ((g / ST) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
                         mbar_arrive_expect_tx(&full_tma[s], Q_BYTES + P_BYTES);
                         tma_load_2d(sQ + s * Q_BYTES, &map_q, &full_tma[s], kb * BK, t0);
+                        tma_load_2d(sQ + s * Q_BYTES + QR * BK, &map_q, &full_tma[s], kb * BK, t0 + SUB);
                         tma_load_3d(sP + s * P_BYTES, &map_p, &full_tma[s], kb * (BK / 2), w0, tl.e);
                     }
                 }
@@ -321,10 +321,13 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     }
                 }
             }
-        } else if (warp == 1) {
-            // ---------------- MMA issuer (even CTA) ----------------
+        } else if (warp < 3) {
+            // ---------------- MMA issuers (even CTA): one half of the tokens each ----------------
             if (leader && lane == 0) {
-                const uint64_t qdesc0 = sw128_desc(smem_u32(sQ)), edesc0 = sw128_desc(smem_u32(sE));
+                const int x = warp - 1;
+                // rows x * QR .. of each CTA's token tile are this half
+                const uint64_t qdesc0 = sw128_desc(smem_u32(sQ) + static_cast<uint32_t>(x * QR * BK));
+                const uint64_t edesc0 = sw128_desc(smem_u32(sE));
                 Tiles<NT> tiles(plan, a.E, a.N);
                 Tile tl;
                 uint32_t g = 0, h = 0;  // K blocks and groups so far
@@ -339,26 +342,29 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         const uint64_t qdesc = qdesc0 + static_cast<uint64_t>((s1 * Q_BYTES) >> 4);
                         const uint64_t edesc = edesc0 + static_cast<uint64_t>((s2 * E_BYTES) >> 4);
                         const bool opens = PER <= 4 || (kb & 1) == 0;
+                        const bool closes = PER <= 4 || (kb & 1) != 0 || kb + 1 == nkb;
 #pragma unroll
                         for (int f = 0; f < FPB; ++f) {
-                            const int b = h & 1;
+                            const int b = 2 * x + (h & 1);
                             if (opens && !wait_bar(&acc_empty[b], ((h >> 1) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
                             if (f == 0 && !wait_bar(&full_exp[s2], (g / SE) & 1u, abort_flag, a.status)) { ok = false; break; }
                             tc_fence_after();
-                            const uint32_t d = tmem_base + static_cast<uint32_t>(b * NT);
+                            const uint32_t d = tmem_base + static_cast<uint32_t>(b * SUB);
 #pragma unroll
                             for (int kk = f * 4 / FPB; kk < (f + 1) * 4 / FPB; ++kk)
                                 mma_i8_pair(d, edesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)),
-                                            qdesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)), idesc<NT>(),
+                                            qdesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)), idesc<SUB>(),
                                             kk == f * 4 / FPB && opens ? 0u : 1u);
-                            if (f + 1 < FPB) commit_both(&acc_full[b]);
-                            if (PER <= 4 || (kb & 1) != 0 || kb + 1 == nkb) ++h;
+                            if (closes) {
+                                commit_both(&acc_full[b]);
+                                ++h;
+                            }
                         }
                         if (ok) commit_both(&mma_done[s1]);
                     }
                 }
-                commit_self(drain);
-                drain_bar(drain, 0);
+                commit_self(&drain[x]);
+                drain_bar(&drain[x], 0);
             }
         } else if (warp >= 4) {
             // ---------------- expanders: own 128 weight rows ----------------
@@ -387,63 +393,61 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     } else {
         // ---------------- drain: own 128 weight rows x NT tokens ----------------
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
-        const int quarter = warp & 3, half = (warp - 8) >> 2;
-        float *sx = sX + (warp - 8) * NC;
-        const uint32_t acc_empty_leader = map_to_peer(smem_u32(acc_empty), 0);
-        const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(half * NC);
+        const int quarter = warp & 3, x = (warp - 8) >> 2;
+        float *sx = sX + (warp - 8) * SUB;
+        const uint32_t empty_leader = map_to_peer(smem_u32(acc_empty + 2 * x), 0);
+        const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(2 * x * SUB);
+        const int groups = static_cast<int>((a.K - 1) >> a.gshift) + 1;
+        const int ends = PER == 8 ? (nkb + 1) / 2 : nkb * FPB;  // groups of the whole K blocks
         Tiles<NT> tiles(plan, a.E, a.N);
         Tile tl;
-        const int groups = static_cast<int>((a.K - 1) >> a.gshift) + 1;
-        uint32_t g = 0, h = 0, full0 = 0, full1 = 0;  // K blocks, groups, and completions of acc_full so far
+        uint32_t h = 0;  // groups so far
         bool ok = true;
         while (ok && tiles.next(tl)) {
             const int n = tl.w0 + static_cast<int>(rank) * kRows + quarter * 32 + lane;
             const bool row_on = n < a.N;
-            const int64_t s_at = tl.e * a.sstride + static_cast<int64_t>(n) * a.lds;
-            const int row0 = tl.row0 + half * NC;  // this warp's first token
+            const ScaleRow<SB> scales(a.s_g, tl.e * a.sstride + static_cast<int64_t>(row_on ? n : 0) * a.lds);
+            const int row0 = tl.row0 + x * SUB;  // this warp's first token
             const int left = tl.hi - row0;
             // the factor 16 of the shifted codes leaves with the token scale
 #pragma unroll
-            for (int i = lane; i < NC; i += 32) sx[i] = i < left ? __fmul_rn(ld_act_f32(a.s_x + row0 + i), 0.0625f) : 0.0f;
+            for (int i = lane; i < SUB; i += 32) sx[i] = i < left ? __fmul_rn(ld_act_f32(a.s_x + row0 + i), 0.0625f) : 0.0f;
             __syncwarp();
-            float2 acc[NC / 2];
+            float2 acc[SUB / 2];
 #pragma unroll
-            for (int j = 0; j < NC / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            float s_next = row_on ? gs_scale(a.s_g, s_at, a.s_bf16) : 0.0f;
-            int gr = 0;  // group of the row
-            for (int kb = 0; ok && kb < nkb; ++kb, ++g) {
-                if (PER == 8 && (kb & 1) == 0 && kb + 1 < nkb) continue;  // the group goes on
-#pragma unroll
-                for (int f = 0; f < FPB; ++f, ++gr) {
-                    const int b = h & 1;
-                    const float s = s_next;
-                    s_next = gr + 1 < groups && row_on ? gs_scale(a.s_g, s_at + gr + 1, a.s_bf16) : 0.0f;
-                    uint64_t *full = f + 1 == FPB ? &mma_done[g % ST] : &acc_full[b];
-                    const uint32_t phase = f + 1 == FPB ? g / ST : b == 0 ? full0++ : full1++;
-                    ++h;
+            for (int j = 0; j < SUB / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
+            float s_next = scales.at(0);
+            for (int gr = 0; gr < ends; ++gr, ++h) {
+                const uint32_t b = h & 1;
+                const float s = s_next;
+                s_next = scales.at(gr + 1 < groups ? gr + 1 : 0);
+                // usually complete: one poll by the whole warp, without a
+                // branch into the waiting loop or a shuffle of its result
+                if (!__all_sync(0xffffffffu, mbar_try_wait(&acc_full[2 * x + b], (h >> 1) & 1u))) {
                     int ready = 0;
-                    if (lane == 0) ready = wait_bar(full, phase & 1u, abort_flag, a.status) ? 1 : 0;
-                    ready = __shfl_sync(0xffffffffu, ready, 0);
-                    if (!ready) { ok = false; break; }
-                    tc_fence_after();
+                    if (lane == 0) ready = wait_bar(&acc_full[2 * x + b], (h >> 1) & 1u, abort_flag, a.status) ? 1 : 0;
+                    ok = __shfl_sync(0xffffffffu, ready, 0) != 0;
+                    if (!ok) break;
+                }
+                tc_fence_after();
 #pragma unroll
-                    for (int c = 0; c < NC / 32; ++c) {
-                        uint32_t v[32];
-                        tmem_ld_32cols(tacc + static_cast<uint32_t>(b * NT + c * 32), v);
-                        if (c == NC / 32 - 1) {
-                            // the buffer is in registers: the next group may use it
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_remote(acc_empty_leader + static_cast<uint32_t>(b * 8));
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], s, v[2 * j], v[2 * j + 1]);
+                for (int c = 0; c < SUB / 32; ++c) {
+                    uint32_t v[32];
+                    tmem_ld_32cols(tacc + b * SUB + static_cast<uint32_t>(c * 32), v);
+                    if (c == SUB / 32 - 1) {
+                        // the sums are in registers: the next group may use the buffer
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_remote(empty_leader + b * 8);
                     }
+                    // groups past the row's last hold zero sums
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], s, v[2 * j], v[2 * j + 1]);
                 }
             }
             if (ok && row_on) {
-                if (a.y_bf16) store_columns<__nv_bfloat16, NC>(a.y, a.ldy, row0, n, left, smem_u32(sx), acc);
-                else store_columns<float, NC>(a.y, a.ldy, row0, n, left, smem_u32(sx), acc);
+                if (a.y_bf16) store_columns<__nv_bfloat16, SUB>(a.y, a.ldy, row0, n, left, smem_u32(sx), acc);
+                else store_columns<float, SUB>(a.y, a.ldy, row0, n, left, smem_u32(sx), acc);
             }
             __syncwarp();
         }
@@ -462,25 +466,25 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 
 // Pairs that can be resident at once, found (with the shared-memory attribute
 // set) on the first launch on each device.
-template <int NT, int PER>
+template <int NT, int PER, bool SB>
 int resident_pairs(int dev)
 {
     constexpr size_t smem = smem_bytes<NT>();
     static_assert(smem <= 232448, "shared memory budget");
     static PerDevice pairs;
     return pairs.get(dev, [&] {
-        if (cudaFuncSetAttribute(gs_gemm_kernel<NT, PER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        if (cudaFuncSetAttribute(gs_gemm_kernel<NT, PER, SB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(smem)) != cudaSuccess)
             return 0;
         // the register split needs all of the launch's registers
         cudaFuncAttributes at;
-        if (cudaFuncGetAttributes(&at, gs_gemm_kernel<NT, PER>) != cudaSuccess || at.numRegs < kLaunchRegs) return 0;
+        if (cudaFuncGetAttributes(&at, gs_gemm_kernel<NT, PER, SB>) != cudaSuccess || at.numRegs < kLaunchRegs) return 0;
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * static_cast<unsigned>(device_sm_count() / 2));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = smem;
         int n = 0;
-        return cudaOccupancyMaxActiveClusters(&n, gs_gemm_kernel<NT, PER>, &cfg) == cudaSuccess ? n : 0;
+        return cudaOccupancyMaxActiveClusters(&n, gs_gemm_kernel<NT, PER, SB>, &cfg) == cudaSuccess ? n : 0;
     });
 }
 
@@ -500,34 +504,40 @@ bool make_weight_map(CUtensorMap *map, const GsArgs &a)
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int NT, int PER>
+template <int NT, int PER, bool SB>
 lowbit_status launch(const GsArgs &a, cudaStream_t st)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
-    const int64_t resident = resident_pairs<NT, PER>(dev);
+    const int64_t resident = resident_pairs<NT, PER, SB>(dev);
     if (resident <= 0) return LOWBIT_ERR_CUDA;
     CUtensorMap mq, mp;
     if (!make_map_2d(&mq, a.q, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M), static_cast<uint64_t>(a.ldq), BK,
-                     NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                     NT / 4, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_weight_map(&mp, a))
         return LOWBIT_ERR_CUDA;
     // experts: their row counts are on the device; at most this many token tiles
     const int64_t token_tiles = a.M / NT + (a.offsets != nullptr ? a.E : 1);
     int64_t pairs = token_tiles * ((a.N + 2 * kRows - 1) / (2 * kRows));
     if (pairs > resident) pairs = resident;
-    return launch_pdl(gs_gemm_kernel<NT, PER>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem_bytes<NT>(), st,
+    return launch_pdl(gs_gemm_kernel<NT, PER, SB>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem_bytes<NT>(), st,
                       0, mq, mp, a);
+}
+
+template <int NT, int PER>
+lowbit_status launch_s(const GsArgs &a, cudaStream_t st)
+{
+    return a.s_bf16 ? launch<NT, PER, true>(a, st) : launch<NT, PER, false>(a, st);
 }
 
 template <int NT>
 lowbit_status launch_g(const GsArgs &a, cudaStream_t st)
 {
     switch (a.gshift) {
-    case 5: return launch<NT, 1>(a, st);
-    case 6: return launch<NT, 2>(a, st);
-    case 7: return launch<NT, 4>(a, st);
-    default: return launch<NT, 8>(a, st);
+    case 5: return launch_s<NT, 1>(a, st);
+    case 6: return launch_s<NT, 2>(a, st);
+    case 7: return launch_s<NT, 4>(a, st);
+    default: return launch_s<NT, 8>(a, st);
     }
 }
 
@@ -538,9 +548,7 @@ lowbit_status set_wait_limit_gs(long long cycles) { return tc::set_wait_limit_he
 lowbit_status gs_gemm_launch(const GsArgs &a, cudaStream_t st)
 {
     const int64_t rows = a.offsets != nullptr ? a.M / a.E : a.M;
-    if (rows > 128) return gsg::launch_g<256>(a, st);
-    if (rows > 64) return gsg::launch_g<128>(a, st);
-    return gsg::launch_g<64>(a, st);
+    return rows > 128 ? gsg::launch_g<256>(a, st) : gsg::launch_g<128>(a, st);
 }
 
 }  // namespace lowbit
