@@ -44,7 +44,7 @@ constexpr int kLaunchRegs = 128, kLeanRegs = 64, kDrainRegs = 192;
 static_assert(256 * kLeanRegs + 256 * kDrainRegs <= kThreads * kLaunchRegs, "the split must fit the launch");
 
 template <int NT> __host__ __device__ constexpr int q_bytes() { return NT / 2 * BK; }
-template <int NT> __host__ __device__ constexpr int stages() { return NT == 256 ? 7 : 8; }
+template <int NT> __host__ __device__ constexpr int stages() { return NT == 256 ? 6 : 8; }
 
 // The tiles of a call: token tiles expert after expert, each swept over the
 // weight rows (fastest), so that a round of pairs shares few token tiles and
@@ -55,11 +55,16 @@ struct Plan {
     int32_t start[LOWBIT_MOE_MAX_EXPERTS + 1];  // its first token tile
 };
 
+// Staging of the output, per drain warp: 16 tokens x 32 weight rows, rows
+// padded by 16 bytes (sized for fp32).
+constexpr int kStageTokens = 16;
+constexpr int kStageBytes = kStageTokens * (32 * 4 + 16);
+
 template <int NT>
 __host__ __device__ constexpr size_t smem_bytes()
 {
     return 1024 + static_cast<size_t>(stages<NT>()) * (q_bytes<NT>() + P_BYTES) +
-           static_cast<size_t>(kExpStages) * E_BYTES + kDrainWarps * NT / 2 * sizeof(float) + sizeof(Plan) + 16 +
+           static_cast<size_t>(kExpStages) * E_BYTES + kDrainWarps * (NT / 2 * sizeof(float) + kStageBytes) + sizeof(Plan) + 16 +
            8 * (2 * stages<NT>() + kExpStages + 12);
 }
 
@@ -77,17 +82,26 @@ template <int NT>
 struct Tiles {
     const Plan *plan;
     uint32_t id, total, num_w;
-    int e = 0;
+    int e = 0, dense_rows;
 
-    __device__ __forceinline__ Tiles(const Plan *p, int E, int64_t N) : plan(p)
+    __device__ __forceinline__ Tiles(const Plan *p, const GsArgs &a) : plan(p)
     {
         id = blockIdx.x >> 1;
-        num_w = static_cast<uint32_t>((N + 2 * kRows - 1) / (2 * kRows));
-        total = static_cast<uint32_t>(p->start[E]) * num_w;
+        num_w = static_cast<uint32_t>((a.N + 2 * kRows - 1) / (2 * kRows));
+        total = static_cast<uint32_t>(p->start[a.E]) * num_w;
+        dense_rows = a.offsets == nullptr ? static_cast<int>(a.M) : 0;
     }
     __device__ __forceinline__ bool next(Tile &t)
     {
         if (id >= total) return false;
+        if (dense_rows > 0) {  // no shared-memory round trips
+            t.e = 0;
+            t.row0 = static_cast<int>(id / num_w) * NT;
+            t.hi = dense_rows;
+            t.w0 = static_cast<int>(id % num_w) * (2 * kRows);
+            id += gridDim.x >> 1;
+            return true;
+        }
         const int tt = static_cast<int>(id / num_w);
         while (tt >= plan->start[e + 1]) ++e;
         t.e = e;
@@ -142,19 +156,23 @@ __host__ __device__ constexpr uint32_t idesc()
 
 // The 128 packed rows of a stage into the K-major 128B-swizzled int8 tile:
 // 16 packed bytes (32 codes) per thread and step; loads cover contiguous
-// bytes and the stores of 8 lanes hit 8 bank groups.
+// bytes and the stores of 8 lanes hit 8 bank groups.  A shared-memory round
+// trip takes 100 to 200 cycles beside the MMAs' operand reads, so all four
+// loads are in flight before the first store.
 __device__ __forceinline__ void expand(uint32_t P, uint32_t E, int et)
 {
+    const int r = et >> 2, qd = et & 3;  // rows r, r + 32, r + 64, r + 96: the same swizzle
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = lds128(P + et * 16 + j * 2048);
+    const uint32_t row = E + r * 128;
+    const uint32_t c0 = row + (((2 * qd) ^ (r & 7)) << 4), c1 = row + (((2 * qd + 1) ^ (r & 7)) << 4);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-        const int i = et + 128 * j;
-        const int r = i >> 2, qd = i & 3;
-        const uint4 w = lds128(P + r * 64 + qd * 16);
-        const uint32_t row = E + r * 128;
-        sts128(row + (((2 * qd) ^ (r & 7)) << 4),
-               make_uint4(i4_expand(w.x, 0), i4_expand(w.x, 1), i4_expand(w.y, 0), i4_expand(w.y, 1)));
-        sts128(row + (((2 * qd + 1) ^ (r & 7)) << 4),
-               make_uint4(i4_expand(w.z, 0), i4_expand(w.z, 1), i4_expand(w.w, 0), i4_expand(w.w, 1)));
+        sts128(c0 + j * 4096,
+               make_uint4(i4_expand(w[j].x, 0), i4_expand(w[j].x, 1), i4_expand(w[j].y, 0), i4_expand(w[j].y, 1)));
+        sts128(c1 + j * 4096,
+               make_uint4(i4_expand(w[j].z, 0), i4_expand(w[j].z, 1), i4_expand(w[j].w, 0), i4_expand(w[j].w, 1)));
     }
 }
 
@@ -183,17 +201,16 @@ __device__ __forceinline__ void fma2(float2 &acc, float s, uint32_t v0, uint32_t
 __device__ __forceinline__ void store_as(__nv_bfloat16 *p, float f) { *p = __float2bfloat16_rn(f); }
 __device__ __forceinline__ void store_as(float *p, float f) { *p = f; }
 
-// The thread's weight row n of tokens row0 .. row0 + min(left, NC) - 1: the
-// 32 lanes of a warp hold consecutive n, so a store covers 64 (bf16) or 128
-// consecutive bytes.
+// The warp's 32 weight rows n0 + lane of tokens row0 .. row0 + min(left, NC) - 1.
+// Element stores, 64 (bf16) or 128 bytes per warp and instruction: for the
+// last weight rows, and for outputs without 16-byte alignment.
 template <typename T, int NC>
-__device__ __forceinline__ void store_columns(void *y, int64_t ldy, int row0, int n, int left, uint32_t sx,
-                                              const float2 (&acc)[NC / 2])
+__device__ __forceinline__ void store_elements(T *p, int64_t ldy, int left, uint32_t sx, const float2 (&acc)[NC / 2])
 {
-    T *p = static_cast<T *>(y) + row0 * ldy + n;
 #pragma unroll
     for (int j = 0; j < NC; j += 4) {
         const uint4 x = lds128(sx + j * 4);
+        if (j >= left) break;
         const float f[4] = {__fmul_rn(acc[j / 2].x, __uint_as_float(x.x)), __fmul_rn(acc[j / 2].y, __uint_as_float(x.y)),
                             __fmul_rn(acc[j / 2 + 1].x, __uint_as_float(x.z)),
                             __fmul_rn(acc[j / 2 + 1].y, __uint_as_float(x.w))};
@@ -203,6 +220,62 @@ __device__ __forceinline__ void store_columns(void *y, int64_t ldy, int row0, in
             p += ldy;
         }
     }
+}
+
+// The same through shared memory, 16 tokens at a time, as 16-byte stores of
+// whole token rows: 512 bytes per instruction.  The element stores took 5000
+// cycles per tile of 256 x 256, which nothing overlaps.
+template <typename T, int NC>
+__device__ __forceinline__ void store_staged(T *p, int64_t ldy, int left, uint32_t sx, uint32_t stage, int lane,
+                                             const float2 (&acc)[NC / 2])
+{
+    constexpr int kRow = 32 * sizeof(T) + 16;             // bytes of a staged token
+    constexpr int kPieces = 32 * sizeof(T) / 16;          // 16-byte pieces of it
+    constexpr int kPer = 32 / kPieces;                    // tokens per store instruction
+    const uint32_t mine = stage + static_cast<uint32_t>(lane * sizeof(T));
+    const uint32_t from = stage + static_cast<uint32_t>(lane / kPieces * kRow + lane % kPieces * 16);
+    char *dst = reinterpret_cast<char *>(p + lane / kPieces * ldy) + lane % kPieces * 16;
+#pragma unroll
+    for (int j0 = 0; j0 < NC; j0 += kStageTokens) {
+        if (j0 >= left) break;
+        uint4 xs[kStageTokens / 4];
+#pragma unroll
+        for (int j = 0; j < kStageTokens / 4; ++j) xs[j] = lds128(sx + j0 * 4 + j * 16);
+#pragma unroll
+        for (int j = 0; j < kStageTokens; j += 4) {
+            const uint4 x = xs[j / 4];
+            const float2 a0 = acc[(j0 + j) / 2], a1 = acc[(j0 + j) / 2 + 1];
+            const float f[4] = {__fmul_rn(a0.x, __uint_as_float(x.x)), __fmul_rn(a0.y, __uint_as_float(x.y)),
+                                __fmul_rn(a1.x, __uint_as_float(x.z)), __fmul_rn(a1.y, __uint_as_float(x.w))};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (sizeof(T) == 2) {
+                    const __nv_bfloat16 b = __float2bfloat16_rn(f[i]);
+                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(mine + (j + i) * kRow),
+                                 "h"(*reinterpret_cast<const uint16_t *>(&b)) : "memory");
+                } else {
+                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + (j + i) * kRow), "f"(f[i]) : "memory");
+                }
+            }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kStageTokens / kPer; ++i) {
+            const uint4 v = lds128(from + i * kPer * kRow);
+            if (j0 + i * kPer + lane / kPieces < left) *reinterpret_cast<uint4 *>(dst) = v;
+            dst += kPer * ldy * static_cast<int64_t>(sizeof(T));
+        }
+        __syncwarp();
+    }
+}
+
+template <typename T, int NC>
+__device__ __forceinline__ void store_columns(void *y, int64_t ldy, int64_t row0, int n0, int64_t N, int left, bool vec,
+                                              uint32_t sx, uint32_t stage, int lane, const float2 (&acc)[NC / 2])
+{
+    T *p = static_cast<T *>(y) + row0 * ldy + n0;
+    if (vec && n0 + 32 <= N) store_staged<T, NC>(p, ldy, left, sx, stage, lane, acc);
+    else if (n0 + lane < N) store_elements<T, NC>(p + lane, ldy, left, sx, acc);
 }
 
 // NT tokens per tile; PER MMAs of 32 codes per group (group / 32); SB: bf16 scales.
@@ -223,7 +296,8 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     uint8_t *sE = sQ + ST * Q_BYTES;             // SE expanded tiles, 1024-aligned
     uint8_t *sP = sE + SE * E_BYTES;             // ST packed tiles
     float *sX = reinterpret_cast<float *>(sP + ST * P_BYTES);  // token scales, one copy per drain warp
-    uint64_t *bars = reinterpret_cast<uint64_t *>(sX + kDrainWarps * SUB);
+    uint8_t *sStage = reinterpret_cast<uint8_t *>(sX + kDrainWarps * SUB);  // output staging, per drain warp
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sStage + kDrainWarps * kStageBytes);
     uint64_t *full_tma = bars;                   // a stage's tiles have landed
     uint64_t *mma_done = bars + ST;              // both halves' MMAs on the stage are complete
     uint64_t *full_exp = bars + 2 * ST;          // both CTAs have expanded the stage (even CTA's is used)
@@ -298,7 +372,7 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         if (warp == 0) {
             // ---------------- TMA producer (both CTAs) ----------------
             if (lane == 0) {
-                Tiles<NT> tiles(plan, a.E, a.N);
+                Tiles<NT> tiles(plan, a);
                 Tile tl;
                 uint32_t g = 0;
                 bool ok = true;
@@ -328,7 +402,7 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 // rows x * QR .. of each CTA's token tile are this half
                 const uint64_t qdesc0 = sw128_desc(smem_u32(sQ) + static_cast<uint32_t>(x * QR * BK));
                 const uint64_t edesc0 = sw128_desc(smem_u32(sE));
-                Tiles<NT> tiles(plan, a.E, a.N);
+                Tiles<NT> tiles(plan, a);
                 Tile tl;
                 uint32_t g = 0, h = 0;  // K blocks and groups so far
                 bool ok = true;
@@ -346,8 +420,12 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
                         for (int f = 0; f < FPB; ++f) {
                             const int b = 2 * x + (h & 1);
-                            if (opens && !wait_bar(&acc_empty[b], ((h >> 1) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
-                            if (f == 0 && !wait_bar(&full_exp[s2], (g / SE) & 1u, abort_flag, a.status)) { ok = false; break; }
+                            // both polls before either result is needed
+                            const uint32_t ph_acc = ((h >> 1) & 1u) ^ 1u, ph_exp = (g / SE) & 1u;
+                            const bool acc_on = !opens || mbar_try_wait(&acc_empty[b], ph_acc);
+                            const bool exp_on = f != 0 || mbar_try_wait(&full_exp[s2], ph_exp);
+                            if (!acc_on && !wait_bar(&acc_empty[b], ph_acc, abort_flag, a.status)) { ok = false; break; }
+                            if (!exp_on && !wait_bar(&full_exp[s2], ph_exp, abort_flag, a.status)) { ok = false; break; }
                             tc_fence_after();
                             const uint32_t d = tmem_base + static_cast<uint32_t>(b * SUB);
 #pragma unroll
@@ -371,7 +449,7 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const int et = threadIdx.x - 128;
             const uint32_t p_base = smem_u32(sP), e_base = smem_u32(sE);
             const uint32_t full_exp_leader = map_to_peer(smem_u32(full_exp), 0);
-            Tiles<NT> tiles(plan, a.E, a.N);
+            Tiles<NT> tiles(plan, a);
             Tile tl;
             uint32_t g = 0;
             bool ok = true;
@@ -399,7 +477,8 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(2 * x * SUB);
         const int groups = static_cast<int>((a.K - 1) >> a.gshift) + 1;
         const int ends = PER == 8 ? (nkb + 1) / 2 : nkb * FPB;  // groups of the whole K blocks
-        Tiles<NT> tiles(plan, a.E, a.N);
+        const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy % (a.y_bf16 ? 8 : 4) == 0;
+        Tiles<NT> tiles(plan, a);
         Tile tl;
         uint32_t h = 0;  // groups so far
         bool ok = true;
@@ -417,37 +496,47 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 #pragma unroll
             for (int j = 0; j < SUB / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
             float s_next = scales.at(0);
+            bool polled = mbar_try_wait(&acc_full[2 * x + (h & 1)], (h >> 1) & 1u);
             for (int gr = 0; gr < ends; ++gr, ++h) {
                 const uint32_t b = h & 1;
                 const float s = s_next;
                 s_next = scales.at(gr + 1 < groups ? gr + 1 : 0);
-                // usually complete: one poll by the whole warp, without a
-                // branch into the waiting loop or a shuffle of its result
-                if (!__all_sync(0xffffffffu, mbar_try_wait(&acc_full[2 * x + b], (h >> 1) & 1u))) {
+                // polled by the whole warp during the previous group's
+                // multiply-adds; usually complete
+                if (!__all_sync(0xffffffffu, polled)) {
                     int ready = 0;
                     if (lane == 0) ready = wait_bar(&acc_full[2 * x + b], (h >> 1) & 1u, abort_flag, a.status) ? 1 : 0;
                     ok = __shfl_sync(0xffffffffu, ready, 0) != 0;
                     if (!ok) break;
                 }
                 tc_fence_after();
+                const uint32_t col = tacc + b * SUB;
+                uint32_t v[2][32];
+                tmem_ld_32cols_async(col, v[0]);
 #pragma unroll
                 for (int c = 0; c < SUB / 32; ++c) {
-                    uint32_t v[32];
-                    tmem_ld_32cols(tacc + b * SUB + static_cast<uint32_t>(c * 32), v);
-                    if (c == SUB / 32 - 1) {
+                    tmem_ld_wait(v[c & 1]);
+                    if (c + 1 < SUB / 32) {
+                        // the next columns arrive during these columns' multiply-adds
+                        tmem_ld_32cols_async(col + static_cast<uint32_t>((c + 1) * 32), v[(c + 1) & 1]);
+                    } else {
                         // the sums are in registers: the next group may use the buffer
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_remote(empty_leader + b * 8);
+                        polled = mbar_try_wait(&acc_full[2 * x + (b ^ 1)], ((h + 1) >> 1) & 1u);
                     }
                     // groups past the row's last hold zero sums
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], s, v[2 * j], v[2 * j + 1]);
+                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], s, v[c & 1][2 * j], v[c & 1][2 * j + 1]);
                 }
             }
-            if (ok && row_on) {
-                if (a.y_bf16) store_columns<__nv_bfloat16, SUB>(a.y, a.ldy, row0, n, left, smem_u32(sx), acc);
-                else store_columns<float, SUB>(a.y, a.ldy, row0, n, left, smem_u32(sx), acc);
+            if (ok) {
+                const uint32_t stage = smem_u32(sStage) + static_cast<uint32_t>((warp - 8) * kStageBytes);
+                if (a.y_bf16)
+                    store_columns<__nv_bfloat16, SUB>(a.y, a.ldy, row0, n - lane, a.N, left, vec, smem_u32(sx), stage, lane, acc);
+                else
+                    store_columns<float, SUB>(a.y, a.ldy, row0, n - lane, a.N, left, vec, smem_u32(sx), stage, lane, acc);
             }
             __syncwarp();
         }
