@@ -33,7 +33,7 @@ lowbit_status check_artifact(const void *packed, int64_t ldp, const void *s_g, l
 {
     if (packed == nullptr || s_g == nullptr || !real_type(sdt) || group_shift(group) < 0) return LOWBIT_ERR_INVALID_ARG;
     if (N <= 0 || K <= 0 || N > INT32_MAX) return LOWBIT_ERR_INVALID_ARG;
-    if (K > LOWBIT_GS_MAX_K) return LOWBIT_ERR_UNSUPPORTED;
+    if (K > LOWBIT_GS_MAX_K || N > LOWBIT_GS_MAX_N) return LOWBIT_ERR_UNSUPPORTED;
     if (ldp < static_cast<int64_t>(lowbit_packed_row_bytes(LOWBIT_INT4, K)) || lds < lowbit_gs_groups(K, group))
         return LOWBIT_ERR_INVALID_ARG;
     if (ldp % 16 != 0 || !aligned(packed, 16) || !aligned(s_g, size_of(sdt))) return LOWBIT_ERR_ALIGNMENT;

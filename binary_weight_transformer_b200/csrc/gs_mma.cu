@@ -17,8 +17,16 @@
 // a step may only hold codes of one group: the four lanes of a row exchange
 // words (2 or 4 shuffles per 16 bytes) so that steps and groups line up.
 //
-// A block owns 8*R weight rows; its warps (and, in a cluster, its peers) split
-// K by units, and the fp32 partial tiles are added in a fixed order.
+// A warp owns 8*R weight rows and a range of K.  Decode is bound by latency, so
+// a warp keeps kAhead units of its range on their way (cp.async into a ring of
+// its own: a lane reads back only what it copied itself, so the loop has no
+// barrier, few registers and little code), and K is split until the ranges
+// are short or the SMs are full.  What the warps of a block share is staged once
+// per block while the first weights arrive: the token codes of its K range
+// (with 16 tokens a warp of 8 rows needs four times as many bytes of them as of
+// weights) and the scales.  The warps of a block, and the blocks of a cluster,
+// that share rows add their fp32 tiles in a fixed order, the latter through
+// distributed shared memory.
 #include "gs_internal.cuh"
 #include "tc_common.cuh"
 
@@ -26,8 +34,10 @@ namespace lowbit {
 namespace gsm {
 
 constexpr int kUnit = 128;     // codes of a row per warp step
-constexpr int kMaxWarps = 16;
-constexpr int kMaxSplit = 4;   // blocks of a cluster
+constexpr int kRowWarps = 4;   // warps of a block along the weight rows
+constexpr int kMaxKWarps = 2;  // and along K
+constexpr int kMaxSplit = 8;   // blocks of a cluster, along K
+constexpr int kAhead = 8;      // units of a warp in flight
 
 enum { kG128 = 0, kG64 = 1, kG32 = 2, kG256 = 3 };
 
@@ -41,55 +51,31 @@ __device__ __forceinline__ void mma_s8(int32_t (&c)[4], uint32_t a0, uint32_t a1
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// The low `valid` bytes of a little-endian word.
-__device__ __forceinline__ uint32_t keep_bytes(uint32_t v, int64_t valid)
-{
-    return valid >= 4 ? v : valid <= 0 ? 0u : v & ((1u << (8 * valid)) - 1u);
-}
-
-// Token codes k .. k+15 (k a multiple of 16) and k .. k+7, zero past K.  Rows
-// are readable up to the next multiple of 16 codes.
-__device__ __forceinline__ uint4 q16(const int8_t *row, int64_t k, int64_t K)
-{
-    if (row == nullptr || k >= K) return make_uint4(0, 0, 0, 0);
-    uint4 v = ld_act_ca_u4(row + k);
-    if (k + 16 > K) {
-        v.x = keep_bytes(v.x, K - k);
-        v.y = keep_bytes(v.y, K - k - 4);
-        v.z = keep_bytes(v.z, K - k - 8);
-        v.w = keep_bytes(v.w, K - k - 12);
-    }
-    return v;
-}
-
-__device__ __forceinline__ uint2 q8(const int8_t *row, int64_t k, int64_t K)
-{
-    if (row == nullptr || k >= K) return make_uint2(0, 0);
-    uint2 v;
-    asm volatile("ld.global.ca.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(row + k) : "memory");
-    v.x = keep_bytes(v.x, K - k);
-    v.y = keep_bytes(v.y, K - k - 4);
-    return v;
-}
-
-// The token fragment words of a unit for one token row: step j uses q[2j]
-// (the four codes of the word's low nibbles) and q[2j+1] (the high ones).
+// Bytes between staged token rows of `units` units: the padding puts the
+// rows that one load instruction reads in different banks (a lane reads 16
+// bytes of every 32, or 8 consecutive bytes with groups of 32).
 template <int GM>
-__device__ __forceinline__ void load_tokens(const int8_t *row, int64_t k0, int64_t K, int t, uint32_t (&q)[8])
+__host__ __device__ constexpr int q_stride(int units)
+{
+    return units * kUnit + (GM == kG32 ? 32 : 16);
+}
+
+// The token fragment words of a unit for one staged token row: step j uses
+// q[2j] (the four codes of the word's low nibbles) and q[2j+1] (the high ones).
+template <int GM>
+__device__ __forceinline__ void load_tokens(uint32_t row, int t, uint32_t (&q)[8])
 {
     if constexpr (GM == kG32) {
         // step j: word t of piece j
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const uint2 v = q8(row, k0 + 32 * j + 8 * t, K);
-            q[2 * j] = v.x;
-            q[2 * j + 1] = v.y;
-        }
+        for (int j = 0; j < 4; ++j)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(q[2 * j]), "=r"(q[2 * j + 1])
+                         : "r"(row + static_cast<uint32_t>(32 * j + 8 * t)));
     } else {
         // steps 0,1 and 2,3: two consecutive words each
-        const int64_t a = GM == kG128 || GM == kG256 ? 32 * t : t < 2 ? 32 * t : 32 * (t - 2) + 16;
-        const int64_t b = GM == kG128 || GM == kG256 ? 32 * t + 16 : t < 2 ? 32 * (t + 2) : 32 * t + 16;
-        const uint4 u = q16(row, k0 + a, K), v = q16(row, k0 + b, K);
+        const int a = GM == kG64 && t >= 2 ? 32 * (t - 2) + 16 : 32 * t;
+        const int b = GM == kG64 && t < 2 ? 32 * (t + 2) : 32 * t + 16;
+        const uint4 u = tc::lds128(row + static_cast<uint32_t>(a)), v = tc::lds128(row + static_cast<uint32_t>(b));
         q[0] = u.x, q[1] = u.y, q[2] = u.z, q[3] = u.w;
         q[4] = v.x, q[5] = v.y, q[6] = v.z, q[7] = v.w;
     }
@@ -116,50 +102,98 @@ __device__ __forceinline__ void line_up(uint4 &w, int t)
     w = even ? make_uint4(a.x, s0, a.z, s1) : make_uint4(s0, a.y, s1, a.w);
 }
 
-// TOK: tokens per pass (8, 16 or 32); R: slabs of 8 weight rows.
+// Most units a block stages at once.
+template <int TOK> __host__ __device__ constexpr int max_chunk() { return TOK == 8 ? 48 : TOK == 16 ? 32 : 16; }
+
+// 16 bytes of shared memory from the first n of src, the rest zero.
+__device__ __forceinline__ void copy_some(uint32_t dst, const void *src, int n)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory"); }
+
+// The bits of a scale as loaded: the conversion would wait for each load.
+__device__ __forceinline__ uint32_t scale_bits16(const uint8_t *p)
+{
+    uint16_t h;
+    asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h) : "l"(p));
+    return h;
+}
+__device__ __forceinline__ uint32_t scale_bits32(const uint8_t *p)
+{
+    uint32_t v;
+    asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+// Units of one call and how they are shared out (see launch).
+struct Split {
+    int units;    // of a row
+    int per;      // runs of units per block of a cluster
+    int chunk;    // units staged at once
+    int split;    // blocks of a cluster
+};
+
+// TOK: tokens per pass (8, 16 or 32); R: slabs of 8 weight rows per warp.
 template <int TOK, int GM, int R>
-__global__ void __launch_bounds__(kMaxWarps * 32)
-gs_mma_kernel(const GsArgs a, int64_t units, int split)
+__global__ void __launch_bounds__(kRowWarps * kMaxKWarps * 32, TOK == 32 ? 2 : TOK == 16 ? 3 : 4)
+gs_mma_kernel(const GsArgs a, const Split sp)
 {
     constexpr int MT = TOK == 32 ? 2 : 1;        // 16-token tiles
     constexpr int EL = TOK == 8 ? 2 : 4;         // C elements in use
-    constexpr int UN = TOK == 32 ? 2 : 4;        // units in flight
-    constexpr int kElems = MT * R * EL;          // partial sums per lane
-    constexpr int kRun = GM == kG256 ? 2 : 1;    // consecutive units of one warp
-    extern __shared__ float red[];               // [warps][kElems][32], then [split - 1][kElems * 32]
-    const int warps = blockDim.x >> 5;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kElems = MT * R * EL;          // sums per lane
+    constexpr int kRun = GM == kG256 ? 2 : 1;    // consecutive units that share a scale
+    constexpr int kGroups = GM == kG32 ? 4 : GM == kG64 ? 2 : 1;  // groups of a unit
+    constexpr int kSteps = 4 / kGroups;
+    constexpr int kPair = TOK == 32 ? kRun : 2;
+    constexpr int kRows = 8 * R * kRowWarps;     // weight rows of a block
+    extern __shared__ __align__(16) uint8_t smem[];  // codes, scales, rings; then the sums that are added
+    __shared__ float sx[TOK];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const int rw = warp & (kRowWarps - 1), kw = warp / kRowWarps;
     const int g = lane >> 2, t = lane & 3;
-    const int rank = split > 1 ? static_cast<int>(tc::cluster_rank()) : 0;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.x / split) * (8 * R);
-    const int64_t groups = ((a.K - 1) >> a.gshift) + 1;
-    const int64_t chunks = (a.K + 31) >> 5;      // 16-byte pieces of a row
-    const bool experts = a.offsets != nullptr;
+    const int n_block = static_cast<int>(blockIdx.x) * kRows;
+    const int n0 = n_block + rw * (8 * R);
+    const int rank = blockIdx.y;
+    const int u_lo = rank * sp.per * kRun;       // this block's units
+    const int u_end = u_lo + sp.per * kRun;
+    const int u_hi = u_end < sp.units ? u_end : (sp.units + kRun - 1) / kRun * kRun;
+    const int stride = q_stride<GM>(sp.chunk);
+    const int cgroups = sp.chunk * kGroups / kRun;  // groups staged at once
+    const uint32_t q_base = tc::smem_u32(smem);
+    const uint32_t s_base = q_base + static_cast<uint32_t>(TOK * stride);  // [row warp, slab][group][8 rows]
+    const uint32_t s_mine = s_base + static_cast<uint32_t>(rw * R * cgroups * 32 + t * 8);
+    const uint32_t ring = s_base + static_cast<uint32_t>(kRows * cgroups * 4 + (warp * kAhead * R * 32 + lane) * 16);
 
-    bool waited = a.prefetch == 0;
-    if (waited) pdl_wait();
+    if (a.prefetch == 0) pdl_wait();
     pdl_trigger();
-    int64_t lo = 0, hi = a.M, step = TOK;
+    int64_t lo, hi, step;
     const uint8_t *packed = a.packed;
-    int64_t s_at = 0;
-    if (experts) {
-        gs_expert_rows(a.offsets, blockIdx.y, a.M, lo, hi, a.status);
-        packed += blockIdx.y * a.pstride;
-        s_at = blockIdx.y * a.sstride;
+    const uint8_t *scales = static_cast<const uint8_t *>(a.s_g);
+    const int s_size = a.s_bf16 ? 2 : 4;
+    if (a.offsets != nullptr) {
+        gs_expert_rows(a.offsets, blockIdx.z, a.M, lo, hi, a.status);
+        packed += blockIdx.z * a.pstride;
+        scales += blockIdx.z * a.sstride * s_size;
+        step = TOK;
     } else {
-        lo = static_cast<int64_t>(blockIdx.y) * TOK;
-        step = static_cast<int64_t>(gridDim.y) * TOK;
+        lo = static_cast<int64_t>(blockIdx.z) * TOK;
+        hi = a.M;
+        step = static_cast<int64_t>(gridDim.z) * TOK;
     }
+    // this lane's row and piece of every unit, and the units that hold it
+    const uint8_t *piece[R];
+    int limit[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int n = n0 + 8 * r + g;
+        piece[r] = packed + (n < a.N ? n : 0) * a.ldp + t * 16;
+        limit[r] = n < a.N ? (static_cast<int>((a.K + 31) >> 5) - t + 3) >> 2 : 0;
+    }
+    bool waited = a.prefetch == 0;
 
     for (int64_t tok = lo; tok < hi; tok += step) {
-        const int8_t *row[MT][2];
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t r = tok + 16 * m + 8 * h + g;
-                row[m][h] = r < hi && (TOK > 8 || h == 0) ? a.q + r * a.ldq : nullptr;
-            }
         float acc[MT][R][EL];
 #pragma unroll
         for (int m = 0; m < MT; ++m)
@@ -168,140 +202,285 @@ gs_mma_kernel(const GsArgs a, int64_t units, int split)
 #pragma unroll
                 for (int i = 0; i < EL; ++i) acc[m][r][i] = 0.0f;
 
-        const int stride = warps * split * kRun;
-        for (int64_t u0 = (rank * warps + warp) * kRun; u0 < units; u0 += static_cast<int64_t>(stride) * (UN / kRun)) {
-            uint4 w[UN][R];
-            float sc[UN][R];
+        for (int c0 = u_lo; c0 < u_hi; c0 += sp.chunk) {
+            const int c1 = c0 + sp.chunk < u_hi ? c0 + sp.chunk : u_hi;
+            const int share = ((c1 - c0) / kRun * kRowWarps + warps - 1) / warps * kRun;  // units per K warp
+            const int v0 = c0 + kw * share;
+            const int v1 = v0 + share < c1 ? v0 + share : c1;
+            // this lane's units to fetch: [v0, end); zeros from there on
+            int end[R];
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                const int64_t u = u0 + static_cast<int64_t>(i / kRun) * stride + i % kRun;
+            for (int r = 0; r < R; ++r) end[r] = limit[r] < v1 ? limit[r] : v1;
+            // unit u into its slot (addresses past `end` are not read)
+            auto request = [&](int u) {
+                const uint32_t slot = ring + static_cast<uint32_t>((u & (kAhead - 1)) * (R * 512));
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int64_t n = n0 + 8 * r + g;
-                    const int64_t c = 4 * u + t;
-                    const int64_t grp = (c << 5) >> a.gshift;  // the scale this lane fetches for its row
-                    w[i][r] = n < a.N && c < chunks ? ld_stream_u4(packed + n * a.ldp + c * 16) : make_uint4(0, 0, 0, 0);
-                    sc[i][r] = n < a.N && grp < groups ? gs_scale(a.s_g, s_at + n * a.lds + grp, a.s_bf16) : 0.0f;
+                for (int r = 0; r < R; ++r) copy_some(slot + r * 512, piece[r] + u * 64, u < end[r] ? 16 : 0);
+                copy_commit();
+            };
+            auto request_first = [&] {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) request(v0 + i);
+            };
+            // Token codes: a warp per row, 16 bytes per lane and copy, zeros
+            // past K and for missing tokens.
+            auto stage_codes = [&] {
+                for (int tk = warp; tk < TOK; tk += warps) {
+                    const int k0 = c0 * kUnit + lane * 16;
+                    const int8_t *src = a.q + (tok + tk < hi ? tok + tk : lo) * a.ldq;
+                    const int left = tok + tk < hi ? static_cast<int>(a.K) - k0 : 0;
+                    const uint32_t dst = q_base + static_cast<uint32_t>(tk * stride + lane * 16);
+                    for (int p = 0; p < (c1 - c0) * kUnit - lane * 16; p += 512) {
+                        const int valid = left - p;
+                        copy_some(dst + p, valid > 0 ? src + k0 + p : a.q, valid >= 16 ? 16 : valid > 0 ? valid : 0);
+                    }
                 }
-            }
-            if (!waited) {
+                copy_commit();
+            };
+            // weights first where they may be read before the wait for the previous kernel
+            const bool weights_first = !waited;
+            if (weights_first) {
+                request_first();
                 pdl_wait();
                 waited = true;
             }
-            int32_t c[MT][R][4];
+            if (c0 != u_lo) __syncthreads();  // the last chunk is read
+            stage_codes();
+            if (!weights_first) {
+                request_first();
+            }
+            // Scales: a warp per row, its rows' loads in flight together.
+            const int g_lo = c0 * kGroups / kRun, g_n = (c1 - c0) * kGroups / kRun;
+            const int g_all = static_cast<int>((a.K - 1) >> a.gshift) + 1;
+            for (int i = lane; i < g_n; i += 32) {
+                constexpr int kMost = kRows / kRowWarps;  // rows of a warp
+                const int rows = kRows / warps, rr0 = warp * rows;
+                const bool in_row = g_lo + i < g_all;
+                const int64_t at = (n_block + rr0) * a.lds + g_lo + i;
+                uint32_t f[kMost];
+                if (a.s_bf16) {
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                // a second unit past the end of the row is all zeros
-                const int64_t u = u0 + static_cast<int64_t>(i / kRun) * stride + i % kRun;
-                if (u - i % kRun >= units) break;
-                uint32_t q[MT][2][8];
+                    for (int j = 0; j < kMost; ++j)
+                        f[j] = in_row && j < rows && n_block + rr0 + j < a.N ? scale_bits16(scales + (at + j * a.lds) * 2) : 0u;
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    load_tokens<GM>(row[m][0], u * kUnit, a.K, t, q[m][0]);
-                    if constexpr (TOK > 8) load_tokens<GM>(row[m][1], u * kUnit, a.K, t, q[m][1]);
+                    for (int j = 0; j < kMost; ++j) f[j] <<= 16;
+                } else {
+#pragma unroll
+                    for (int j = 0; j < kMost; ++j)
+                        f[j] = in_row && j < rows && n_block + rr0 + j < a.N ? scale_bits32(scales + (at + j * a.lds) * 4) : 0u;
                 }
 #pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    line_up<GM>(w[i][r], t);
-                    constexpr int kGroups = GM == kG32 ? 4 : GM == kG64 ? 2 : 1;
-                    constexpr int kSteps = 4 / kGroups;
+                for (int j = 0; j < kMost; j += 4)
+                    if (j < rows)
+                        tc::sts128(s_base + static_cast<uint32_t>((((rr0 + j) >> 3) * cgroups + i) * 32 + ((rr0 + j) & 7) * 4),
+                                   make_uint4(f[j], f[j + 1], f[j + 2], f[j + 3]));
+            }
+            // the factor 16 of the shifted codes leaves with the token scale
+            if (c0 == u_lo && threadIdx.x < TOK)
+                sx[threadIdx.x] = tok + threadIdx.x < hi ? __fmul_rn(ld_act_f32(a.s_x + tok + threadIdx.x), 0.0625f) : 0.0f;
+            if (weights_first) copy_wait<0>();
+            else copy_wait<kAhead>();  // the codes; the weights may still be on their way
+            __syncthreads();
+
+            // kPair units at a time: their shared-memory loads and MMA chains overlap
+#pragma unroll 1
+            for (int u0 = v0; u0 < v1; u0 += kPair) {
+                copy_wait<kAhead - kPair>();
+                uint4 x[kPair][R];
+                uint32_t q[kPair][MT][2][8];
 #pragma unroll
-                    for (int gr = 0; gr < kGroups; ++gr) {
-                        // scales of the rows 2t and 2t+1 that this lane's C columns belong to
-                        const float s0 = __shfl_sync(0xffffffffu, sc[i][r], 8 * t + kSteps * gr);
-                        const float s1 = __shfl_sync(0xffffffffu, sc[i][r], 8 * t + 4 + kSteps * gr);
+                for (int i = 0; i < kPair; ++i) {
+                    const uint32_t slot = ring + static_cast<uint32_t>(((u0 + i) & (kAhead - 1)) * (R * 512));
 #pragma unroll
-                        for (int m = 0; m < MT; ++m) {
-                            if (i % kRun == 0) c[m][r][0] = c[m][r][1] = c[m][r][2] = c[m][r][3] = 0;
+                    for (int r = 0; r < R; ++r) x[i][r] = tc::lds128(slot + r * 512);
+                    // (a last odd unit's partner has zero codes)
+                    const uint32_t at = q_base + static_cast<uint32_t>((u0 + i - c0) * kUnit + g * stride);
 #pragma unroll
-                            for (int s = 0; s < kSteps; ++s) {
-                                const int j = gr * kSteps + s;
-                                const uint32_t word = (&w[i][r].x)[j];
-                                mma_s8(c[m][r], q[m][0][2 * j], TOK > 8 ? q[m][1][2 * j] : 0u, q[m][0][2 * j + 1],
-                                       TOK > 8 ? q[m][1][2 * j + 1] : 0u, i4_expand(word, 0), i4_expand(word, 1));
-                            }
-                            if (i % kRun == kRun - 1) {
-#pragma unroll
-                                for (int x = 0; x < EL; ++x)
-                                    acc[m][r][x] = __fmaf_rn(x & 1 ? s1 : s0, __int2float_rn(c[m][r][x]), acc[m][r][x]);
-                            }
-                        }
+                    for (int m = 0; m < MT; ++m) {
+                        load_tokens<GM>(at + static_cast<uint32_t>(16 * m * stride), t, q[i][m][0]);
+                        if constexpr (TOK > 8) load_tokens<GM>(at + static_cast<uint32_t>((16 * m + 8) * stride), t, q[i][m][1]);
                     }
                 }
+#pragma unroll
+                for (int i = 0; i < kPair; ++i) {
+#pragma unroll
+                    for (int r = 0; r < R; ++r) line_up<GM>(x[i][r], t);
+                    request(u0 + i + kAhead);  // the slot is in registers
+                }
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int gr = 0; gr < kGroups; ++gr) {
+                        int32_t c[kPair / kRun][MT][4];
+#pragma unroll
+                        for (int i = 0; i < kPair / kRun; ++i)
+#pragma unroll
+                            for (int m = 0; m < MT; ++m) c[i][m][0] = c[i][m][1] = c[i][m][2] = c[i][m][3] = 0;
+#pragma unroll
+                        for (int st = 0; st < kSteps; ++st)
+#pragma unroll
+                            for (int i = 0; i < kPair; ++i)
+#pragma unroll
+                                for (int m = 0; m < MT; ++m) {
+                                    const int k = gr * kSteps + st;
+                                    const uint32_t word = (&x[i][r].x)[k];
+                                    mma_s8(c[i / kRun][m], q[i][m][0][2 * k], TOK > 8 ? q[i][m][1][2 * k] : 0u,
+                                           q[i][m][0][2 * k + 1], TOK > 8 ? q[i][m][1][2 * k + 1] : 0u, i4_expand(word, 0),
+                                           i4_expand(word, 1));
+                                }
+#pragma unroll
+                        for (int i = 0; i < kPair / kRun; ++i) {
+                            if (u0 + i * kRun >= v1) break;
+                            // scales of the rows 2t and 2t + 1 that this lane's C columns belong to
+                            float s0, s1;
+                            const int gi = (u0 + i * kRun - c0) * kGroups / kRun + gr;
+                            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(s0), "=f"(s1)
+                                         : "r"(s_mine + static_cast<uint32_t>((r * cgroups + gi) * 32)));
+#pragma unroll
+                            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                                for (int e = 0; e < EL; ++e)
+                                    acc[m][r][e] = __fmaf_rn(e & 1 ? s1 : s0, __int2float_rn(c[i][m][e]), acc[m][r][e]);
+                        }
+                    }
             }
-        }
-        if (!waited) {
-            pdl_wait();
-            waited = true;
         }
 
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int i = 0; i < EL; ++i) red[(warp * kElems + (m * R + r) * EL + i) * 32 + lane] = acc[m][r][i];
-        __syncthreads();
-        float *peers = red + warps * kElems * 32;
-        if (split > 1 && rank > 0) {
-            for (int idx = threadIdx.x; idx < kElems * 32; idx += blockDim.x) {
-                float v = 0.0f;
-                for (int w = 0; w < warps; ++w) v += red[w * kElems * 32 + idx];
-                const uint32_t dst = tc::map_to_peer(tc::smem_u32(peers + (rank - 1) * kElems * 32 + idx), 0);
-                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(dst), "f"(v) : "memory");
+        // element e of lane (g, t): token 16 m + g + 8 (e >> 1), row 8 r + 2 t + (e & 1)
+        auto put = [&](int m, int r, int e, int ln, int row0, float v) {
+            const int tk = 16 * m + (ln >> 2) + 8 * (e >> 1);
+            const int n = row0 + 8 * r + 2 * (ln & 3) + (e & 1);
+            if (tok + tk < hi && n < a.N) {
+                const float f = __fmul_rn(v, sx[tk]);
+                if (a.y_bf16) static_cast<__nv_bfloat16 *>(a.y)[(tok + tk) * a.ldy + n] = __float2bfloat16_rn(f);
+                else static_cast<float *>(a.y)[(tok + tk) * a.ldy + n] = f;
             }
-        }
-        if (split > 1) tc::cluster_sync_all();
-        if (rank == 0) {
-            for (int idx = threadIdx.x; idx < kElems * 32; idx += blockDim.x) {
+        };
+        if (sp.split == 1 && warps == kRowWarps) {
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < EL; ++e) put(m, r, e, lane, n0, acc[m][r][e]);
+        } else {
+            __syncthreads();  // the staged codes are read
+            float *sums = reinterpret_cast<float *>(smem);  // [K warp][element][row warp, lane]
+            constexpr int kTile = kElems * kRowWarps * 32;
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int e = 0; e < EL; ++e)
+                        sums[kw * kTile + ((m * R + r) * EL + e) * (kRowWarps * 32) + rw * 32 + lane] = acc[m][r][e];
+            if (sp.split > 1) tc::cluster_sync_all();
+            else __syncthreads();
+            // each block adds its share of the tile: K warps within ranks, ranks in order
+            for (int i = kTile * rank / sp.split + threadIdx.x; i < kTile * (rank + 1) / sp.split; i += blockDim.x) {
+                float part[kMaxSplit][kMaxKWarps];
+#pragma unroll
+                for (int p = 0; p < kMaxSplit; ++p)
+#pragma unroll
+                    for (int k = 0; k < kMaxKWarps; ++k) {
+                        part[p][k] = 0.0f;
+                        if (p < sp.split && k * kRowWarps < warps) {
+                            const uint32_t at = q_base + static_cast<uint32_t>((k * kTile + i) * 4);
+                            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part[p][k])
+                                         : "r"(sp.split > 1 ? tc::map_to_peer(at, static_cast<uint32_t>(p)) : at) : "memory");
+                        }
+                    }
                 float v = 0.0f;
-                for (int w = 0; w < warps; ++w) v += red[w * kElems * 32 + idx];
-                for (int p = 1; p < split; ++p) v += peers[(p - 1) * kElems * 32 + idx];
-                const int e = idx >> 5, ln = idx & 31;
-                const int m = e / (R * EL), r = e / EL % R, x = e % EL;
-                const int64_t token = tok + 16 * m + (ln >> 2) + 8 * (x >> 1);
-                const int64_t n = n0 + 8 * r + 2 * (ln & 3) + (x & 1);
-                if (token < hi && n < a.N) {
-                    // v carries the factor 16 of the shifted codes
-                    const float f = __fmul_rn(v, __fmul_rn(ld_act_f32(a.s_x + token), 0.0625f));
-                    if (a.y_bf16) static_cast<__nv_bfloat16 *>(a.y)[token * a.ldy + n] = __float2bfloat16_rn(f);
-                    else static_cast<float *>(a.y)[token * a.ldy + n] = f;
-                }
+#pragma unroll
+                for (int p = 0; p < kMaxSplit; ++p)
+#pragma unroll
+                    for (int k = 0; k < kMaxKWarps; ++k) v += part[p][k];
+                const int e = i / (kRowWarps * 32), th = i % (kRowWarps * 32);
+                put(e / (R * EL), e / EL % R, e % EL, th & 31, n_block + (th >> 5) * (8 * R), v);
             }
+            if (sp.split > 1) tc::cluster_sync_all();  // peers have read this block's sums
         }
-        if (split > 1) tc::cluster_sync_all();
-        else __syncthreads();
+        if (tok + step < hi) __syncthreads();  // before sx and the codes are staged again
     }
     if (!waited) pdl_wait();
+}
+
+// As launch_pdl, with clusters of `split` blocks along y.
+template <typename... KArgs, typename... Args>
+lowbit_status launch_clusters_y(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
+                                unsigned split, Args &&...args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = 1;
+    attr[1].val.clusterDim.y = split;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = split > 1 ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) != cudaSuccess) return LOWBIT_ERR_CUDA;
+    return launch_status();
 }
 
 template <int TOK, int GM, int R>
 lowbit_status launch(const GsArgs &a, cudaStream_t st)
 {
+    constexpr int kRows = 8 * R * kRowWarps;
     constexpr int kElems = (TOK == 32 ? 2 : 1) * R * (TOK == 8 ? 2 : 4);
+    constexpr int kRun = GM == kG256 ? 2 : 1;
+    constexpr int kGroups = GM == kG32 ? 4 : GM == kG64 ? 2 : 1;
     const int64_t units = (a.K + kUnit - 1) / kUnit;
-    const int64_t slabs = (a.N + 8 * R - 1) / (8 * R);
-    int64_t ytiles, active;
+    const int64_t runs = (units + kRun - 1) / kRun;
+    const int64_t slabs = (a.N + kRows - 1) / kRows;
+    int64_t ztiles, active;
     if (a.offsets != nullptr) {
-        ytiles = a.E;
+        ztiles = a.E;
         active = a.E < a.M ? a.E : a.M;
     } else {
-        ytiles = (a.M + TOK - 1) / TOK;
-        if (ytiles > 65535) ytiles = 65535;
-        active = ytiles;
+        ztiles = (a.M + TOK - 1) / TOK;
+        if (ztiles > 65535) ztiles = 65535;
+        active = ztiles;
     }
-    // Warps per slab: enough for about 32 on every SM, at most one per
-    // unit (pair of units).
-    const int64_t want = static_cast<int64_t>(device_sm_count()) * 32;
-    int64_t warps = 1, split = 1;
-    const int64_t runs = GM == kG256 ? (units + 1) / 2 : units;
-    while (warps < 8 && slabs * active * warps < want && warps * 2 <= runs) warps *= 2;
-    while (split < kMaxSplit && slabs * active * warps * split < want && warps * split * 2 <= runs) split *= 2;
-    if (slabs * split > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
-    const size_t smem = static_cast<size_t>(warps + split - 1) * kElems * 32 * 4;
-    return launch_pdl(gs_mma_kernel<TOK, GM, R>, dim3(static_cast<unsigned>(slabs * split), static_cast<unsigned>(ytiles)),
-                      dim3(static_cast<unsigned>(warps * 32)), smem, st,
-                      split > 1 ? static_cast<unsigned>(split) : 0u, a, units, static_cast<int>(split));
+    // Ranges of K per row block: as many as make a warp's range about four
+    // units, as long as all warps are resident at once.
+    const int64_t fit = static_cast<int64_t>(device_sm_count()) * (TOK == 8 ? 32 : TOK == 16 ? 24 : 16) / (slabs * active * kRowWarps);
+    int64_t ranges = (units + 3) / 4;
+    if (ranges > fit) ranges = fit;
+    if (ranges > runs) ranges = runs;
+    const int64_t kwarps = ranges < 2 ? 1 : kMaxKWarps;
+    int64_t split = ranges / kwarps;
+    if (split < 1) split = 1;
+    if (split > kMaxSplit) split = kMaxSplit;
+    const int64_t per = (runs + split - 1) / split;
+    split = (runs + per - 1) / per;
+    if (slabs > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
+    const int64_t chunk = per * kRun < max_chunk<TOK>() ? per * kRun : max_chunk<TOK>();
+    const auto bytes = [](int64_t units_, int64_t kwarps_) {
+        return static_cast<size_t>(TOK) * q_stride<GM>(static_cast<int>(units_)) +
+               static_cast<size_t>(kRows * units_ * kGroups / kRun * 4) + kRowWarps * kwarps_ * kAhead * R * 512;
+    };
+    size_t smem = bytes(chunk, kwarps);
+    const size_t sums = static_cast<size_t>(kElems) * kRowWarps * kwarps * 32 * 4;
+    if (smem < sums) smem = sums;
+    static PerDevice configured;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
+    if (configured.get(dev, [&] {
+            return cudaFuncSetAttribute(gs_mma_kernel<TOK, GM, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(bytes(max_chunk<TOK>(), kMaxKWarps))) == cudaSuccess ? 1 : 0;
+        }) <= 0)
+        return LOWBIT_ERR_CUDA;
+    const Split sp = {static_cast<int>(units), static_cast<int>(per), static_cast<int>(chunk), static_cast<int>(split)};
+    return launch_clusters_y(gs_mma_kernel<TOK, GM, R>,
+                             dim3(static_cast<unsigned>(slabs), static_cast<unsigned>(split), static_cast<unsigned>(ztiles)),
+                             dim3(static_cast<unsigned>(kRowWarps * kwarps * 32)), smem, st, static_cast<unsigned>(split), a,
+                             sp);
 }
 
 template <int TOK, int R>

@@ -469,10 +469,11 @@ lowbit_status lowbit_rescale(const int32_t *acc, int64_t ldacc, int64_t M, int64
  * decodes them); instead of one scale per row there is one per `group`
  * consecutive codes of a row, group in {32, 64, 128, 256}: s_g [N, lds]
  * fp32 or bf16 (sdt), entry (n, g) for codes g*group .. g*group + group - 1.
- * The last group of a row may be short.  K <= LOWBIT_GS_MAX_K, else
- * LOWBIT_ERR_UNSUPPORTED.
+ * The last group of a row may be short.  K <= LOWBIT_GS_MAX_K and
+ * N <= LOWBIT_GS_MAX_N, else LOWBIT_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 #define LOWBIT_GS_MAX_K 1048576
+#define LOWBIT_GS_MAX_N 1073741824
 
 /* Groups of a row, ceil(K / group); 0 for bad arguments. */
 int64_t lowbit_gs_groups(int64_t K, int group);

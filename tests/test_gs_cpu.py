@@ -24,7 +24,7 @@ BAD_ARTIFACT = [
     (dict(group=0), INVALID), (dict(group=48), INVALID), (dict(group=512), INVALID), (dict(group=-32), INVALID),
     (dict(ldp=112), INVALID), (dict(lds=1), INVALID), (dict(ldp=136), ALIGN), (dict(packed=FAKE + 8), ALIGN),
     (dict(s_g=FAKE + 2), ALIGN), (dict(s_g=FAKE + 1, sdt=bwt.BF16), ALIGN), (dict(K=0), INVALID), (dict(N=0), INVALID),
-    (dict(K=-5), INVALID), (dict(N=2**31), INVALID), (dict(K=bwt.GS_MAX_K + 1), UNSUPPORTED),
+    (dict(K=-5), INVALID), (dict(N=2**31), INVALID), (dict(K=bwt.GS_MAX_K + 1, ldp=2**20), UNSUPPORTED), (dict(N=2**30 + 1), UNSUPPORTED),
 ]
 
 
