@@ -444,9 +444,10 @@ def lowbit_rescale(acc, s_x, s_w, fmt: int, out_dtype: int = F32, y=None, status
 # 4-bit weights with group scales, and expert layers
 #
 # These calls take a few microseconds on the device for small inputs, so the
-# checks below are written for the host's time: one expression per tensor,
-# the current stream's handle without a Stream object (which takes 3 us), and
-# the details of a refusal worked out only when there is one.
+# checks below are written for the host's time: one expression per tensor, no
+# strides asked of a contiguous one, the current stream's handle without a
+# Stream object (which takes 3 us), and the details of a refusal worked out
+# only when there is one.
 # ---------------------------------------------------------------------------
 class _Torch:
     """torch and what the calls below need of it, looked up at the first call."""
@@ -454,7 +455,8 @@ class _Torch:
     def __init__(self):
         import torch
         self.torch, self.empty = torch, torch.empty
-        self.i8, self.u8, self.i32, self.f32 = torch.int8, torch.uint8, torch.int32, torch.float32
+        self.i8, self.u8, self.i32, self.i64, self.f32 = (torch.int8, torch.uint8, torch.int32, torch.int64,
+                                                          torch.float32)
         self.kind = {torch.float32: F32, torch.bfloat16: BF16}  # lowbit_dtype of a real type
         self.real = {F32: torch.float32, BF16: torch.bfloat16}
         self.device = torch.cuda.current_device
@@ -472,30 +474,64 @@ def _tt() -> _Torch:
     return _torch_names
 
 
-def _takes(t, what: str, dim: int, dtype, dev: int | None = None) -> int:
-    """The checks the C side cannot make: a CUDA tensor of this rank, type and
-    (when given) device, with unit stride along the last dimension.  Returns
-    the device index."""
-    d = t.get_device()
-    if t.ndim != dim or t.dtype != dtype or d < 0 or (dev is not None and d != dev) or \
-            (t.stride(-1) != 1 and t.shape[-1] > 1):
-        if t.ndim != dim:
-            raise ValueError(f"{what} must have {dim} dimension(s), got shape {tuple(t.shape)}")
-        if t.dtype != dtype:
-            raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
-        if d < 0:
-            raise ValueError(f"{what} must be a CUDA tensor")
-        if dev is not None and d != dev:
-            raise ValueError(f"{what} is on cuda:{d}, the call's other tensors on cuda:{dev}")
+def _refuse(t, what: str, dim: int, dtype, dev: int):
+    """The reason why a tensor was not taken."""
+    if t.ndim != dim:
+        raise ValueError(f"{what} must have {dim} dimension(s), got shape {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    raise ValueError(f"{what} is on {t.device}, the call's other tensors on cuda:{dev}")
+
+
+def _strides(t, what: str) -> int:
+    """Row stride of a tensor that is not contiguous, whose last dimension must
+    have unit stride (a dimension of one entry has no stride that counts)."""
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{what} must have unit stride along its last dimension")
-    return d
+    return t.stride(-2) if t.shape[-2] > 1 else max(t.stride(-2), t.shape[-1])
 
 
-def _kind(t, what: str) -> int:
-    """The lowbit_dtype of an fp32 or bf16 tensor."""
-    k = _tt().kind.get(t.dtype)
+def _vector(t, what: str, n: int, dtype, dev: int):
+    """Checks a contiguous vector of n entries."""
+    if t.ndim != 1 or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, what, 1, dtype, dev)
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous [{n}], got shape {tuple(t.shape)}")
+
+
+def _slots(t, what: str, dtype, T: int, k: int, dev: int):
+    """Checks a contiguous [T, k] table."""
+    if t.ndim != 2 or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, what, 2, dtype, dev)
+    if t.shape != (T, k) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous [{T}, {k}], got shape {tuple(t.shape)}")
+
+
+def _rows(t, what: str, rows: int, cols: int, dtype, dev: int) -> int:
+    """Checks a [rows, cols] matrix; its row stride."""
+    if t.ndim != 2 or t.dtype is not dtype or t.get_device() != dev:
+        _refuse(t, what, 2, dtype, dev)
+    if t.shape != (rows, cols):
+        raise ValueError(f"{what} must be [{rows}, {cols}], got {tuple(t.shape)}")
+    return cols if t.is_contiguous() else _strides(t, what)
+
+
+def _matrix(t, what: str, dtype):
+    """A matrix on some CUDA device: (device, rows, columns, row stride)."""
+    dev = t.get_device()
+    if t.ndim != 2 or t.dtype is not dtype or dev < 0:
+        _refuse(t, what, 2, dtype, dev)
+    rows, cols = t.shape
+    return dev, rows, cols, cols if t.is_contiguous() else _strides(t, what)
+
+
+def _kind(dtype, what: str) -> int:
+    """The lowbit_dtype of a real torch type."""
+    k = _tt().kind.get(dtype)
     if k is None:
-        raise TypeError(f"{what} must be float32 or bfloat16, got {t.dtype}")
+        raise TypeError(f"{what} must be float32 or bfloat16, got {dtype}")
     return k
 
 
@@ -506,49 +542,18 @@ def _real(kind: int, what: str):
     return dt
 
 
-def _ld(t, dim: int = 0) -> int:
-    """Row stride of t: its stride along `dim`, or at least the row length
-    where that dimension has one entry (whose stride says nothing)."""
-    return t.stride(dim) if t.shape[dim] > 1 else max(t.stride(dim), t.shape[-1])
-
-
-def _slots(t, what: str, dtype, T: int, k: int, dev: int):
-    _takes(t, what, 2, dtype, dev)
-    if t.shape[0] != T or t.shape[1] != k or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous [{T}, {k}], got {tuple(t.shape)}")
-
-
-def _output(y, what: str, rows: int, cols: int, kind: int, dev: int):
-    dt = _real(kind, "the output type")
-    if y is None:
-        return _tt().empty((rows, cols), dtype=dt, device=dev)
-    _takes(y, what, 2, dt, dev)
-    if y.shape[0] != rows or y.shape[1] != cols:
-        raise ValueError(f"{what} must be [{rows}, {cols}], got {tuple(y.shape)}")
-    return y
-
-
-def _vector(t, what: str, n: int, dtype, dev: int):
-    if t is None:
-        return _tt().empty(n, dtype=dtype, device=dev)
-    _takes(t, what, 1, dtype, dev)
-    if t.shape[0] != n:
-        raise ValueError(f"{what} must be [{n}], got {tuple(t.shape)}")
-    return t
-
-
 def _call(name: str, dev: int, status, stream, *args):
     """One ABI call with the tensors' device current and, by default, on that
     device's current stream."""
-    tt = _tt()
+    tt = _torch_names
     if tt.device() != dev:
         with tt.torch.cuda.device(dev):
             return _call(name, dev, status, stream, *args)
     if status is not None:
-        _takes(status, "status", 1, tt.i32, dev)
+        _vector(status, "status", 1, tt.i32, dev)
         status = status.data_ptr()
     st = getattr(_lib or lib(), name)(*args, status, tt.stream(dev) if stream is None else stream.cuda_stream)
-    if st != OK:
+    if st:
         raise LowbitError(st, name)
 
 
@@ -564,74 +569,67 @@ def lowbit_gs_pack(w, group: int = 128, scale_dtype: int = F32, packed=None, s_g
     """Quantise and pack w[N, K] (fp32 or bf16) into 4-bit codes with one
     scale per `group` codes of a row (see lowbit.h).  Returns packed
     [N, ldp] uint8 and s_g [N, ceil(K / group)] of the scale type.  Every
-    byte of a packed row is written, so rows must be contiguous."""
-    kind = _kind(w, "w")
-    dev = _takes(w, "w", 2, w.dtype)
-    N, K = w.shape
-    G = gs_groups(K, group)
+    byte of a packed row is written, so its rows must be contiguous."""
     tt = _tt()
+    kind, sdt = _kind(w.dtype, "w"), _real(scale_dtype, "scale_dtype")
+    dev, N, K, ldw = _matrix(w, "w", w.dtype)
+    G = gs_groups(K, group)
     if packed is None:
         packed = tt.empty((N, ldp if ldp is not None else (K + 31) // 32 * 16), dtype=tt.u8, device=dev)
-    else:
-        _takes(packed, "packed", 2, tt.u8, dev)
-        if packed.shape[0] != N or not packed.is_contiguous():
-            raise ValueError(f"packed must be contiguous with {N} rows")
-    s_g = _output(s_g, "s_g", N, G, scale_dtype, dev)
-    _call("lowbit_gs_pack", dev, status, stream, w.data_ptr(), kind, N, K, _ld(w), group, packed.data_ptr(),
-          packed.shape[1], s_g.data_ptr(), scale_dtype, _ld(s_g))
+    elif _matrix(packed, "packed", tt.u8)[:2] != (dev, N) or not packed.is_contiguous():
+        raise ValueError(f"packed must be contiguous with {N} rows on cuda:{dev}")
+    if s_g is None:
+        s_g = tt.empty((N, G), dtype=sdt, device=dev)
+    lds = _rows(s_g, "s_g", N, G, sdt, dev)
+    _call("lowbit_gs_pack", dev, status, stream, w.data_ptr(), kind, N, K, ldw, group, packed.data_ptr(),
+          packed.shape[1], s_g.data_ptr(), scale_dtype, lds)
     return packed, s_g
-
-
-def _artifact(packed, s_g, K: int, group: int, dim: int, dev: int) -> int:
-    """Checks of an artifact and its scales (rows, or experts and rows, in
-    front); the scales' lowbit_dtype."""
-    kind = _kind(s_g, "s_g")
-    _takes(packed, "packed", dim, _tt().u8, dev)
-    _takes(s_g, "s_g", dim, s_g.dtype, dev)
-    p, s = packed.shape, s_g.shape
-    if p[-1] < (K + 7) // 8 * 4:
-        raise ValueError(f"packed rows hold {p[-1]} bytes, K = {K} needs {(K + 7) // 8 * 4}")
-    if s[-1] != gs_groups(K, group) or s[:-1] != p[:-1]:
-        raise ValueError(f"s_g must be {(*p[:-1], gs_groups(K, group))}, got {tuple(s)}")
-    return kind
 
 
 def lowbit_gs_unpack(packed, s_g, K: int, group: int = 128, out_dtype: int = F32, w=None, status=None, stream=None):
     """The values code * scale of a group-scaled artifact, [N, K]."""
-    dev = packed.get_device()
-    kind = _artifact(packed, s_g, K, group, 2, dev)
-    N = packed.shape[0]
-    w = _output(w, "w", N, K, out_dtype, dev)
-    _call("lowbit_gs_unpack", dev, status, stream, packed.data_ptr(), _ld(packed), s_g.data_ptr(), kind, _ld(s_g), N, K,
-          group, w.data_ptr(), out_dtype, _ld(w))
+    tt = _tt()
+    dt, kind = _real(out_dtype, "out_dtype"), _kind(s_g.dtype, "s_g")
+    dev, N, width, ldp = _matrix(packed, "packed", tt.u8)
+    _fits(width, K)
+    lds = _rows(s_g, "s_g", N, gs_groups(K, group), s_g.dtype, dev)
+    if w is None:
+        w = tt.empty((N, K), dtype=dt, device=dev)
+    ldw = _rows(w, "w", N, K, dt, dev)
+    _call("lowbit_gs_unpack", dev, status, stream, packed.data_ptr(), ldp, s_g.data_ptr(), kind, lds, N, K, group,
+          w.data_ptr(), out_dtype, ldw)
     return w
 
 
-def _token_codes(q, s_x, K):
-    tt = _tt()
-    dev = _takes(q, "q", 2, tt.i8)
-    _takes(s_x, "s_x", 1, tt.f32, dev)
-    M, width = q.shape
-    if K is None:
-        K = width
-    if not 0 < K <= width:
-        raise ValueError(f"q rows hold {width} codes, K = {K}")
-    if s_x.shape[0] != M:
-        raise ValueError(f"s_x must be [{M}], got {tuple(s_x.shape)}")
-    return dev, M, K
+def _fits(width: int, K: int):
+    if not 0 < (K + 7) // 8 * 4 <= width:
+        raise ValueError(f"packed rows hold {width} bytes, K = {K} needs {(K + 7) // 8 * 4}")
 
 
 def lowbit_gs_linear(q, s_x, packed, s_g, group: int = 128, out_dtype: int = F32, K: int | None = None, y=None,
                      status=None, stream=None, weights_stable: bool = False):
     """y[M, N] from int8 codes q[M, >=K] and a group-scaled artifact packed
     [N, ldp], s_g [N, ceil(K / group)] (see lowbit.h); y is fp32 or bf16."""
-    dev, M, K = _token_codes(q, s_x, K)
-    kind = _artifact(packed, s_g, K, group, 2, dev)
-    N = packed.shape[0]
-    y = _output(y, "y", M, N, out_dtype, dev)
-    _call("lowbit_gs_linear", dev, status, stream, q.data_ptr(), _ld(q), s_x.data_ptr(), M, K, packed.data_ptr(),
-          _ld(packed), s_g.data_ptr(), kind, _ld(s_g), group, N, y.data_ptr(), out_dtype, _ld(y),
-          WEIGHTS_STABLE if weights_stable else 0)
+    tt = _tt()
+    dt, kind = _real(out_dtype, "out_dtype"), _kind(s_g.dtype, "s_g")
+    dev, M, codes, ldq = _matrix(q, "q", tt.i8)
+    if K is None:
+        K = codes
+    elif not 0 < K <= codes:
+        raise ValueError(f"q rows hold {codes} codes, K = {K}")
+    _vector(s_x, "s_x", M, tt.f32, dev)
+    on, N, width, ldp = _matrix(packed, "packed", tt.u8)
+    if on != dev:
+        _refuse(packed, "packed", 2, tt.u8, dev)
+    _fits(width, K)
+    lds = _rows(s_g, "s_g", N, gs_groups(K, group), s_g.dtype, dev)
+    if y is None:
+        y = tt.empty((M, N), dtype=dt, device=dev)
+        ldy = N
+    else:
+        ldy = _rows(y, "y", M, N, dt, dev)
+    _call("lowbit_gs_linear", dev, status, stream, q.data_ptr(), ldq, s_x.data_ptr(), M, K, packed.data_ptr(), ldp,
+          s_g.data_ptr(), kind, lds, group, N, y.data_ptr(), out_dtype, ldy, WEIGHTS_STABLE if weights_stable else 0)
     return y
 
 
@@ -640,15 +638,41 @@ def lowbit_gs_linear_experts(q, s_x, offsets, packed, s_g, group: int = 128, out
     """lowbit_gs_linear with expert weights packed [E, N, ldp], s_g
     [E, N, ceil(K / group)]: expert e takes rows offsets[e] .. offsets[e+1]-1
     of q.  Rows of y behind offsets[E] are left as they were."""
-    dev, R, K = _token_codes(q, s_x, K)
-    kind = _artifact(packed, s_g, K, group, 3, dev)
-    E, N = packed.shape[:2]
-    _vector(offsets, "offsets", E + 1, _tt().i32, dev)
-    y = _output(y, "y", R, N, out_dtype, dev)
-    ldp, lds = _ld(packed, 1), _ld(s_g, 1)
-    _call("lowbit_gs_linear_experts", dev, status, stream, q.data_ptr(), _ld(q), s_x.data_ptr(), R, K,
-          offsets.data_ptr(), E, packed.data_ptr(), ldp, packed.stride(0) if E > 1 else N * ldp, s_g.data_ptr(), kind,
-          lds, s_g.stride(0) if E > 1 else N * lds, group, N, y.data_ptr(), out_dtype, _ld(y))
+    tt = _tt()
+    dt, kind = _real(out_dtype, "out_dtype"), _kind(s_g.dtype, "s_g")
+    dev, R, codes, ldq = _matrix(q, "q", tt.i8)
+    if K is None:
+        K = codes
+    elif not 0 < K <= codes:
+        raise ValueError(f"q rows hold {codes} codes, K = {K}")
+    _vector(s_x, "s_x", R, tt.f32, dev)
+    if packed.ndim != 3 or packed.dtype is not tt.u8 or packed.get_device() != dev:
+        _refuse(packed, "packed", 3, tt.u8, dev)
+    if s_g.ndim != 3 or s_g.get_device() != dev:
+        _refuse(s_g, "s_g", 3, s_g.dtype, dev)
+    E, N, width = packed.shape
+    _fits(width, K)
+    G = gs_groups(K, group)
+    if s_g.shape != (E, N, G):
+        raise ValueError(f"s_g must be [{E}, {N}, {G}], got {tuple(s_g.shape)}")
+    _vector(offsets, "offsets", E + 1, tt.i32, dev)
+    if packed.is_contiguous():
+        ldp, pstride = width, N * width
+    else:
+        ldp = _strides(packed, "packed")
+        pstride = packed.stride(0) if E > 1 else N * ldp
+    if s_g.is_contiguous():
+        lds, sstride = G, N * G
+    else:
+        lds = _strides(s_g, "s_g")
+        sstride = s_g.stride(0) if E > 1 else N * lds
+    if y is None:
+        y = tt.empty((R, N), dtype=dt, device=dev)
+        ldy = N
+    else:
+        ldy = _rows(y, "y", R, N, dt, dev)
+    _call("lowbit_gs_linear_experts", dev, status, stream, q.data_ptr(), ldq, s_x.data_ptr(), R, K, offsets.data_ptr(),
+          E, packed.data_ptr(), ldp, pstride, s_g.data_ptr(), kind, lds, sstride, group, N, y.data_ptr(), out_dtype, ldy)
     return y
 
 
@@ -657,20 +681,22 @@ def lowbit_moe_plan(experts, E: int, offsets=None, pos=None, status=None, stream
     negative: dropped) by expert.  Returns offsets [E + 1] and pos [T, k], the
     row of each slot in expert order (-1 for a dropped one), both int32."""
     tt = _tt()
-    wide = experts.dtype != tt.i32
-    if wide and experts.dtype != tt.torch.int64:
-        raise TypeError(f"experts must be int32 or int64, got {experts.dtype}")
-    dev = _takes(experts, "experts", 2, experts.dtype)
+    dtype = experts.dtype
+    if dtype is not tt.i32 and dtype is not tt.i64:
+        raise TypeError(f"experts must be int32 or int64, got {dtype}")
+    dev, T, k, _ = _matrix(experts, "experts", dtype)
     if not experts.is_contiguous():
         raise ValueError("experts must be contiguous")
-    T, k = experts.shape
-    offsets = _vector(offsets, "offsets", E + 1, tt.i32, dev)
+    if offsets is None:
+        offsets = tt.empty(E + 1, dtype=tt.i32, device=dev)
+    else:
+        _vector(offsets, "offsets", E + 1, tt.i32, dev)
     if pos is None:
         pos = tt.empty((T, k), dtype=tt.i32, device=dev)
     else:
         _slots(pos, "pos", tt.i32, T, k, dev)
-    _call("lowbit_moe_plan", dev, status, stream, experts.data_ptr(), 1 if wide else 0, T, k, E, offsets.data_ptr(),
-          pos.data_ptr())
+    _call("lowbit_moe_plan", dev, status, stream, experts.data_ptr(), 1 if dtype is tt.i64 else 0, T, k, E,
+          offsets.data_ptr(), pos.data_ptr())
     return offsets, pos
 
 
@@ -680,25 +706,29 @@ def lowbit_moe_gather(x, pos, s_x=None, out=None, s_out=None, status=None, strea
     scales s_x[T] when given.  Returns out, or (out, s_out) with s_x.  The
     gradient is lowbit_moe_combine(d_out, pos)."""
     tt = _tt()
-    dev = _takes(x, "x", 2, x.dtype)
-    T, width = x.shape
+    dtype = x.dtype
+    dev, T, width, ldx = _matrix(x, "x", dtype)
     k = pos.shape[-1]
     _slots(pos, "pos", tt.i32, T, k, dev)
     if out is None:
-        out = tt.empty((T * k, width), dtype=x.dtype, device=dev)
+        rows, ldo = T * k, width
+        out = tt.empty((rows, width), dtype=dtype, device=dev)
     else:
-        _takes(out, "out", 2, x.dtype, dev)
-        if out.shape[1] != width:
-            raise ValueError(f"out must have rows of {width}, got {tuple(out.shape)}")
-    rows = out.shape[0]
+        rows = out.shape[0]
+        ldo = _rows(out, "out", rows, width, dtype, dev)
+    from_s = to_s = None
     if s_x is not None:
         _vector(s_x, "s_x", T, tt.f32, dev)
-        s_out = _vector(s_out, "s_out", rows, tt.f32, dev)
+        if s_out is None:
+            s_out = tt.empty(rows, dtype=tt.f32, device=dev)
+        else:
+            _vector(s_out, "s_out", rows, tt.f32, dev)
+        from_s, to_s = s_x.data_ptr(), s_out.data_ptr()
     elif s_out is not None:
         raise ValueError("s_out needs s_x")
-    b = x.element_size()
-    _call("lowbit_moe_gather", dev, status, stream, x.data_ptr(), width * b, _ld(x) * b, _ptr(s_x), pos.data_ptr(), T,
-          k, out.data_ptr(), _ld(out) * b, _ptr(s_out), rows)
+    b = dtype.itemsize
+    _call("lowbit_moe_gather", dev, status, stream, x.data_ptr(), width * b, ldx * b, from_s, pos.data_ptr(), T, k,
+          out.data_ptr(), ldo * b, to_s, rows)
     return out if s_x is None else (out, s_out)
 
 
@@ -707,16 +737,22 @@ def lowbit_moe_combine(ys, pos, weights=None, y=None, status=None, stream=None):
     ys[pos[t, j]] (fp32 or bf16 rows, fp32 sums); without weights the plain
     sum, which is the gradient of lowbit_moe_gather."""
     tt = _tt()
-    kind = _kind(ys, "ys")
-    dev = _takes(ys, "ys", 2, ys.dtype)
-    R, K = ys.shape
+    dtype = ys.dtype
+    kind = _kind(dtype, "ys")
+    dev, R, K, ldys = _matrix(ys, "ys", dtype)
     T, k = pos.shape
     _slots(pos, "pos", tt.i32, T, k, dev)
+    w = None
     if weights is not None:
         _slots(weights, "weights", tt.f32, T, k, dev)
-    y = _output(y, "y", T, K, kind, dev)
-    _call("lowbit_moe_combine", dev, status, stream, ys.data_ptr(), kind, _ld(ys), R, pos.data_ptr(), _ptr(weights), T,
-          k, K, y.data_ptr(), _ld(y))
+        w = weights.data_ptr()
+    if y is None:
+        y = tt.empty((T, K), dtype=dtype, device=dev)
+        ldy = K
+    else:
+        ldy = _rows(y, "y", T, K, dtype, dev)
+    _call("lowbit_moe_combine", dev, status, stream, ys.data_ptr(), kind, ldys, R, pos.data_ptr(), w, T, k, K,
+          y.data_ptr(), ldy)
     return y
 
 
@@ -724,21 +760,24 @@ def lowbit_moe_combine_backward(dy, ys, pos, weights, d_ys=None, d_w=None, statu
     """Gradients of lowbit_moe_combine: d_ys like ys (rows no slot names are
     left as they were) and d_w [T, k] fp32."""
     tt = _tt()
-    kind = _kind(dy, "dy")
-    dev = _takes(dy, "dy", 2, dy.dtype)
-    _takes(ys, "ys", 2, dy.dtype, dev)
-    (T, k), (R, K) = pos.shape, ys.shape
-    if dy.shape[0] != T or dy.shape[1] != K:
-        raise ValueError(f"dy must be [{T}, {K}], got {tuple(dy.shape)}")
+    dtype = ys.dtype
+    kind = _kind(dtype, "ys")
+    dev, R, K, ldys = _matrix(ys, "ys", dtype)
+    T, k = pos.shape
+    lddy = _rows(dy, "dy", T, K, dtype, dev)
     _slots(pos, "pos", tt.i32, T, k, dev)
     _slots(weights, "weights", tt.f32, T, k, dev)
-    d_ys = _output(d_ys, "d_ys", R, K, kind, dev)
+    if d_ys is None:
+        d_ys = tt.empty((R, K), dtype=dtype, device=dev)
+        ldd = K
+    else:
+        ldd = _rows(d_ys, "d_ys", R, K, dtype, dev)
     if d_w is None:
         d_w = tt.empty((T, k), dtype=tt.f32, device=dev)
     else:
         _slots(d_w, "d_w", tt.f32, T, k, dev)
-    _call("lowbit_moe_combine_backward", dev, status, stream, dy.data_ptr(), _ld(dy), ys.data_ptr(), _ld(ys), kind, R,
-          pos.data_ptr(), weights.data_ptr(), T, k, K, d_ys.data_ptr(), _ld(d_ys), d_w.data_ptr())
+    _call("lowbit_moe_combine_backward", dev, status, stream, dy.data_ptr(), lddy, ys.data_ptr(), ldys, kind, R,
+          pos.data_ptr(), weights.data_ptr(), T, k, K, d_ys.data_ptr(), ldd, d_w.data_ptr())
     return d_ys, d_w
 
 

@@ -258,3 +258,35 @@ def test_layer_in_a_graph_and_on_another_stream(M):
             got[i].append(bwt.lowbit_gs_linear(q, s_x, packed, s, 64, stream=st, y=torch.empty_like(want)))
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for half in got for g in half)
+
+
+def test_wrappers_refuse_on_the_gpu():
+    """Shapes, strides and types of CUDA tensors that the C side cannot see."""
+    q, s_x = (cuda(a) for a in tokens(1, 4, 64))
+    packed, s = bwt.lowbit_gs_pack(cuda(weights(1, 8, 64)), 32)
+    for args, kw, err in (((q, s_x[:3], packed, s, 32), {}, ValueError), ((q, s_x, packed, s, 64), {}, ValueError),
+                          ((q, s_x, packed, s, 48), {}, ValueError), ((q, s_x, packed, s, 32), dict(K=65), ValueError),
+                          ((q, s_x, packed, s, 32), dict(K=0), ValueError),
+                          ((q, s_x, packed[:, :16], s, 32), {}, ValueError),
+                          ((q, s_x, packed, s.half(), 32), {}, TypeError), ((q, s_x.double(), packed, s, 32), {}, TypeError),
+                          ((q, s_x, packed, s, 32, bwt.I32), {}, ValueError),
+                          ((q, s_x, packed, s, 32), dict(y=torch.empty(4, 9, device="cuda")), ValueError),
+                          ((q, s_x, packed, s, 32), dict(y=torch.empty(8, 4, device="cuda").T), ValueError),
+                          ((q, s_x, packed, s, 32), dict(status=torch.zeros(2, dtype=torch.int32, device="cuda")), ValueError),
+                          ((q[:, ::2], s_x, packed, s, 32), dict(K=16), ValueError),
+                          ((q, s_x, packed.cpu(), s, 32), {}, ValueError)):
+        with pytest.raises(err):
+            bwt.lowbit_gs_linear(*args, **kw)
+    with pytest.raises(bwt.LowbitError):  # rows of codes that overlap
+        bwt.lowbit_gs_linear(q[:1].expand(4, 64), s_x, packed, s, 32)
+    with pytest.raises(ValueError):  # packed rows of a wider buffer
+        bwt.lowbit_gs_pack(cuda(weights(1, 8, 64)), 32, packed=torch.empty(8, 64, dtype=torch.uint8, device="cuda")[:, :32])
+    pos = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        bwt.lowbit_moe_gather(q, pos[:3])
+    with pytest.raises(ValueError):
+        bwt.lowbit_moe_gather(q, pos, s_out=s_x)
+    with pytest.raises(TypeError):
+        bwt.lowbit_moe_combine(q, pos)
+    with pytest.raises(ValueError):
+        bwt.lowbit_moe_combine(s, pos, torch.ones(4, 4, device="cuda")[:, ::2])

@@ -129,24 +129,27 @@ def test_python_refuses_before_any_call():
     """CPU tensors, wrong types, shapes and strides raise in the wrapper."""
     f, i8, u8, i32 = torch.float32, torch.int8, torch.uint8, torch.int32
     z = lambda *s, d=f: torch.zeros(*s, dtype=d)  # noqa: E731
-    with pytest.raises(ValueError, match="CUDA"):
-        bwt.lowbit_gs_pack(z(4, 64))
-    with pytest.raises(ValueError, match="dimension"):
-        bwt.lowbit_gs_pack(z(64))
-    with pytest.raises(TypeError, match="int8"):
-        bwt.lowbit_gs_linear(z(2, 64), z(2), z(4, 32, d=u8), z(4, 2), 32)
-    with pytest.raises(ValueError, match="CUDA"):
-        bwt.lowbit_gs_linear(z(2, 64, d=i8), z(2), z(4, 32, d=u8), z(4, 2), 32)
-    with pytest.raises(ValueError, match="CUDA"):
-        bwt.lowbit_moe_plan(z(4, 2, d=i32), 8)
-    with pytest.raises(ValueError, match="dimension"):
-        bwt.lowbit_moe_plan(z(4, d=i32), 8)
-    with pytest.raises(ValueError, match="CUDA"):
-        bwt.lowbit_moe_gather(z(4, 8), z(4, 2, d=i32))
-    with pytest.raises(ValueError, match="CUDA"):
-        bwt.lowbit_moe_combine(z(8, 8), z(4, 2, d=i32))
-    with pytest.raises(ValueError, match="CUDA"):
-        bwt.lowbit_moe_combine_backward(z(4, 8), z(8, 8), z(4, 2, d=i32), z(4, 2))
+    for call in (lambda: bwt.lowbit_gs_pack(z(4, 64)),
+                 lambda: bwt.lowbit_gs_unpack(z(4, 32, d=u8), z(4, 2), 64, 32),
+                 lambda: bwt.lowbit_gs_linear(z(2, 64, d=i8), z(2), z(4, 32, d=u8), z(4, 2), 32),
+                 lambda: bwt.lowbit_gs_linear_experts(z(2, 64, d=i8), z(2), z(2, d=i32), z(1, 4, 32, d=u8), z(1, 4, 2), 32),
+                 lambda: bwt.lowbit_moe_plan(z(4, 2, d=i32), 8), lambda: bwt.lowbit_moe_gather(z(4, 8), z(4, 2, d=i32)),
+                 lambda: bwt.lowbit_moe_combine(z(8, 8), z(4, 2, d=i32)),
+                 lambda: bwt.lowbit_moe_combine_backward(z(4, 8), z(8, 8), z(4, 2, d=i32), z(4, 2))):
+        with pytest.raises(ValueError, match="CUDA"):
+            call()
+    for call in (lambda: bwt.lowbit_gs_pack(z(64)), lambda: bwt.lowbit_moe_plan(z(4, d=i32), 8),
+                 lambda: bwt.lowbit_moe_gather(z(4), z(4, 2, d=i32))):
+        with pytest.raises(ValueError, match="dimension"):
+            call()
+    for call, name in ((lambda: bwt.lowbit_gs_linear(z(2, 64), z(2), z(4, 32, d=u8), z(4, 2), 32), "int8"),
+                       (lambda: bwt.lowbit_gs_pack(z(4, 64, d=torch.float16)), "float16"),
+                       (lambda: bwt.lowbit_moe_plan(z(4, 2), 8), "int32 or int64"),
+                       (lambda: bwt.lowbit_moe_combine(z(4, 2, d=torch.float64), z(2, 2, d=i32)), "float64")):
+        with pytest.raises(TypeError, match=name):
+            call()
+    with pytest.raises(ValueError, match="F32 or BF16"):
+        bwt.lowbit_gs_pack(z(4, 64), 32, bwt.I32)
 
 
 def test_reference_packing_round_trip():
