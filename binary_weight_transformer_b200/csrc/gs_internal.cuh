@@ -60,6 +60,21 @@ __device__ __forceinline__ void gs_expert_rows(const int32_t *offsets, int e, in
     if (hi < lo) hi = lo;
 }
 
+// id = quotient * d + remainder.  A 64-bit division is about a hundred
+// instructions, more than many of these kernels do with what it addresses, so
+// values that fit 32 bits take the short one.
+__device__ __forceinline__ void divide(int64_t id, int64_t d, int64_t &quotient, int64_t &remainder)
+{
+    if (((static_cast<uint64_t>(id) | static_cast<uint64_t>(d)) >> 32) == 0) {
+        const uint32_t q = static_cast<uint32_t>(id) / static_cast<uint32_t>(d);
+        quotient = q;
+        remainder = static_cast<uint32_t>(id) - q * static_cast<uint32_t>(d);
+    } else {
+        quotient = id / d;
+        remainder = id % d;
+    }
+}
+
 lowbit_status gs_mma_launch(const GsArgs &a, cudaStream_t st);
 lowbit_status gs_gemm_launch(const GsArgs &a, cudaStream_t st);
 lowbit_status gs_pack_launch(const void *w, int w_bf16, int64_t N, int64_t K, int64_t ldw, int gshift, uint8_t *packed,

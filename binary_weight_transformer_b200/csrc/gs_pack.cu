@@ -9,14 +9,19 @@
 // per lane, which is one packed word per lane, one 128-byte store per warp and
 // whole groups (32 to 256 codes = 4 to 32 lanes) whose maximum is a few
 // shuffles.  32 (fp32) or 16 (bf16) bytes per lane in flight at full occupancy
-// cover the memory latency without unrolling.
+// cover the memory latency; what held the packer back was instructions (25 per
+// weight at first: 64-bit divisions for the address, an IEEE division and
+// reciprocal per lane).  A lane's eight fp32 values are
+// one 32-byte access where rows allow it: as two of 16 bytes, every 32-byte
+// sector crosses the L2 twice.
 #include "gs_internal.cuh"
 
 namespace lowbit {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnit = 256;  // codes per warp
+constexpr int kUnit = 256;  // codes per warp and piece
+constexpr int kInFlight = 4;  // words per thread of a large unpack
 
 // The code of one weight by the definition, whatever the scale's size.
 // qf = RN(a / s) is monotone in the exact quotient and every half is a float,
@@ -54,13 +59,9 @@ __device__ __forceinline__ void load8(const void *w, int64_t at, int valid, bool
                 v[i] = __uint_as_float((i & 1) ? (x & 0xffff0000u) : (x << 16));
             }
         } else {
-            const uint4 u0 = ld_act_u4(static_cast<const float *>(w) + at);
-            const uint4 u1 = ld_act_u4(static_cast<const float *>(w) + at + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = __uint_as_float((&u0.x)[i]);
-                v[4 + i] = __uint_as_float((&u1.x)[i]);
-            }
+            asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                         : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                         : "l"(static_cast<const float *>(w) + at) : "memory");
         }
         return;
     }
@@ -77,68 +78,98 @@ __device__ __forceinline__ void load8(const void *w, int64_t at, int valid, bool
     }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kThreads)
-gs_pack_kernel(const void *__restrict__ w, int64_t N, int64_t K, int64_t ldw, int vec, int gshift, int64_t units,
-               uint8_t *__restrict__ packed, int64_t ldp, void *__restrict__ s_g, int s_bf16, int64_t lds,
-               int32_t *status)
+// RN(a / 7).  Markstein's correction (IBM J. Res. Dev. 34, 1990): with y =
+// RN(1/7) and q = RN(a y), the residual r = a - 7 q is exact in one fma and
+// RN(q + r y) is the correctly rounded quotient, where nothing underflows.
+__device__ __forceinline__ float seventh(float a)
 {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t unit = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
-    if (unit >= N * units) return;
-    const int64_t n = unit / units;
-    const int64_t k0 = (unit % units) * kUnit + lane * 8;
-    const int64_t left = K - k0;
-    const int valid = left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0;
+    if (a < 0x1p-100f) return __fdiv_rn(a, 7.0f);
+    constexpr float y = 1.0f / 7.0f;
+    const float q = __fmul_rn(a, y);
+    return __fmaf_rn(__fmaf_rn(-7.0f, q, a), y, q);
+}
 
-    float v[8];
-    load8<BF16>(w, n * ldw + k0, valid, vec != 0, v);
+// The packed word of a lane's eight weights, and (from the first lane of each
+// group of `lanes`) its scale.
+template <bool S16, int lanes>
+__device__ __forceinline__ uint32_t pack_word(const float (&v)[8], int lane, bool owns, void *s_at,
+                                              int32_t *status)
+{
     uint32_t top = 0;  // |w| as bits: non-finite values sort above finite ones
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-    const int lanes = (1 << gshift) >> 3;
+#pragma unroll
     for (int o = 1; o < lanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (!finite_bits(top)) {
-        if ((lane & (lanes - 1)) == 0) report(status, LOWBIT_ERR_NONFINITE);
+    const bool first = (lane & (lanes - 1)) == 0;
+    if (first && !finite_bits(top)) report(status, LOWBIT_ERR_NONFINITE);
+    float s = seventh(__uint_as_float(top));
+    if constexpr (S16) {
+        const __nv_bfloat16 b = __float2bfloat16_rn(s);
+        s = __bfloat162float(b);
+        if (first && owns) *static_cast<__nv_bfloat16 *>(s_at) = b;
+    } else {
+        if (first && owns) *static_cast<float *>(s_at) = s;
     }
-    float s = __fdiv_rn(__uint_as_float(top), 7.0f);
-    const __nv_bfloat16 sb = __float2bfloat16_rn(s);
-    if (s_bf16) s = __bfloat162float(sb);
-    if ((lane & (lanes - 1)) == 0 && k0 < K) {
-        const int64_t at = n * lds + (k0 >> gshift);
-        if (s_bf16) static_cast<__nv_bfloat16 *>(s_g)[at] = sb;
-        else static_cast<float *>(s_g)[at] = s;
-    }
-
-    uint32_t word = 0;
     if (s >= 0x1p-60f && s <= 0x1p+60f) {
-        // u = RN(w * RN(1/s)) is within 7.03 * 2^-23 < 1e-6 of the exact
-        // quotient, so both round to the same integer unless u is that near
-        // a half; about one weight in 10^5 is, and goes by the definition.
+        // u = RN(w * c), c within 2^-23 of 1/s (rcp.approx: 1 ulp), is within
+        // 7.03 * 1.5 * 2^-23 < 1.3e-6 of the exact quotient, so both round to
+        // the same integer unless u is that near a half; where one of eight
+        // weights is within 1e-5 (one lane in 10^4), all go by the definition.
         // The rounding is the addition of 1.5 * 2^23, whose low bits are then
         // the code in two's complement.  |u| <= 7.03: a bf16 scale is at most
         // 2^-8 below the quotient, so no clip.
-        const float c = __frcp_rn(s);
+        float c;
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(s));
+        float m[8], far = 0.0f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float u = __fmul_rn(v[i], c);
-            const float m = __fadd_rn(u, 12582912.0f);
-            uint32_t code = __float_as_uint(m);
-            if (fabsf(__fsub_rn(u, __fsub_rn(m, 12582912.0f))) > 0.49999f)
-                code = static_cast<uint32_t>(code_exact(v[i], s));
-            word |= (code & 15u) << (8 * (i & 3) + 4 * (i >> 2));
+            m[i] = __fadd_rn(u, 12582912.0f);
+            far = fmaxf(far, fabsf(__fsub_rn(u, __fsub_rn(m[i], 12582912.0f))));
         }
-    } else if (s > 0.0f) {
+        if (far > 0.49999f) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = __int_as_float(code_exact(v[i], s));
+        }
+        // low bytes of four codes each, then their low nibbles side by side
+        uint32_t four[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t a = __byte_perm(__float_as_uint(m[4 * h]), __float_as_uint(m[4 * h + 1]), 0x0040);
+            const uint32_t b = __byte_perm(__float_as_uint(m[4 * h + 2]), __float_as_uint(m[4 * h + 3]), 0x0040);
+            four[h] = __byte_perm(a, b, 0x5410);
+        }
+        return (four[0] & 0x0f0f0f0fu) | ((four[1] << 4) & 0xf0f0f0f0u);
+    }
+    uint32_t word = 0;
+    if (s > 0.0f) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             word |= (static_cast<uint32_t>(code_exact(v[i], s)) & 15u) << (8 * (i & 3) + 4 * (i >> 2));
     }
+    return word;
+}
+
+template <bool BF16, bool S16, int GS>
+__global__ void __launch_bounds__(kThreads, 8)
+gs_pack_kernel(const void *__restrict__ w, int64_t N, int64_t K, int64_t ldw, int vec, int64_t units,
+               uint8_t *__restrict__ packed, int64_t ldp, uint8_t *__restrict__ s_g, int64_t lds, int32_t *status)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31;
+    int64_t n, at;
+    divide(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), units, n, at);
+    if (n >= N) return;
+    const int64_t k0 = at * kUnit + lane * 8;
+    const int64_t left = K - k0;
+    float v[8];
+    load8<BF16>(w, n * ldw + k0, left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0, vec != 0, v);
+    const uint32_t word = pack_word<S16, (1 << GS) / 8>(v, lane, left > 0, s_g + (n * lds + (k0 >> GS)) * (S16 ? 2 : 4), status);
     if (k0 / 2 < ldp) *reinterpret_cast<uint32_t *>(packed + n * ldp + k0 / 2) = word;
 }
 
-template <bool BF16>
+template <bool BF16, int U>
 __global__ void __launch_bounds__(kThreads)
 gs_unpack_kernel(const uint8_t *__restrict__ packed, int64_t ldp, const void *__restrict__ s_g, int s_bf16,
                  int64_t lds, int64_t N, int64_t K, int gshift, int64_t words, void *__restrict__ w, int64_t ldw,
@@ -146,58 +177,110 @@ gs_unpack_kernel(const uint8_t *__restrict__ packed, int64_t ldp, const void *__
 {
     pdl_wait();
     pdl_trigger();
-    const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (idx >= N * words) return;
-    const int64_t n = idx / words;
-    const int64_t wi = idx % words;
-    const uint32_t word = ld_act_u32(packed + n * ldp + wi * 4);
-    const int64_t k0 = wi * 8;
-    const int64_t at = n * lds + (k0 >> gshift);
-    const float s = s_bf16 ? __uint_as_float(static_cast<uint32_t>(
-                                 ld_act_u16(static_cast<const uint16_t *>(s_g) + at)) << 16)
-                           : ld_act_f32(static_cast<const float *>(s_g) + at);
-    const int valid = K - k0 >= 8 ? 8 : static_cast<int>(K - k0);
-    bool bad = false;
-    float v[8];
+    uint32_t word[U], scale[U];
+    int64_t row[U], k0s[U];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int bit = 8 * (i & 3) + 4 * (i >> 2);
-        int c = static_cast<int>(word << (28 - bit)) >> 28;
-        if (c == -8 || (i >= valid && c != 0)) {
-            bad = true;
-            c = 0;
+    for (int u = 0; u < U; ++u) {
+        const int64_t idx = (static_cast<int64_t>(blockIdx.x) * U + u) * kThreads + threadIdx.x;
+        int64_t wi;
+        divide(idx, words, row[u], wi);
+        k0s[u] = wi * 8;
+        word[u] = scale[u] = 0;
+        if (row[u] < N) {
+            word[u] = ld_act_u32(packed + row[u] * ldp + wi * 4);
+            const int64_t at = row[u] * lds + (k0s[u] >> gshift);
+            if (s_bf16) scale[u] = ld_act_u16(static_cast<const uint16_t *>(s_g) + at);
+            else scale[u] = ld_act_u32(static_cast<const float *>(s_g) + at);
         }
-        v[i] = __fmul_rn(static_cast<float>(c), s);
+    }
+    bool bad = false;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        if (row[u] >= N) break;
+        const float s = __uint_as_float(s_bf16 ? scale[u] << 16 : scale[u]);
+        const int64_t n = row[u], k0 = k0s[u];
+        const int valid = K - k0 >= 8 ? 8 : static_cast<int>(K - k0);
+        // bits no code of the row owns, and reserved fields: a nibble 1000 is a
+        // zero nibble of x, which the subtraction's borrow marks
+        uint32_t codes = word[u];
+        const uint32_t x = codes ^ 0x88888888u;
+        if (((x - 0x11111111u) & ~x & 0x88888888u) != 0u || valid < 8) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t field = 15u << (8 * (i & 3) + 4 * (i >> 2));
+                if ((codes & field) == (field & 0x88888888u) || (i >= valid && (codes & field) != 0u)) {
+                    bad = true;
+                    codes &= ~field;
+                }
+            }
+        }
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = __fmul_rn(static_cast<float>(static_cast<int>(codes << (28 - 8 * (i & 3) - 4 * (i >> 2))) >> 28), s);
+        if (valid == 8 && vec) {
+            if constexpr (BF16) {
+                uint4 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+                    (&o.x)[i] = *reinterpret_cast<const uint32_t *>(&p);
+                }
+                *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w) + n * ldw + k0) = o;
+            } else {
+                asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};"
+                             ::"l"(static_cast<float *>(w) + n * ldw + k0), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]),
+                               "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]) : "memory");
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (i < valid) {
+                    if constexpr (BF16) static_cast<__nv_bfloat16 *>(w)[n * ldw + k0 + i] = __float2bfloat16_rn(v[i]);
+                    else static_cast<float *>(w)[n * ldw + k0 + i] = v[i];
+                }
+            }
+        }
     }
     if (bad) report(status, LOWBIT_ERR_RESERVED_CODE);
-    if (valid == 8 && vec) {
-        if constexpr (BF16) {
-            uint4 u;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 p = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                (&u.x)[i] = *reinterpret_cast<const uint32_t *>(&p);
-            }
-            *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(w) + n * ldw + k0) = u;
-        } else {
-            float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(w) + n * ldw + k0);
-            dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-            dst[1] = make_float4(v[4], v[5], v[6], v[7]);
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        if (i < valid) {
-            if constexpr (BF16) static_cast<__nv_bfloat16 *>(w)[n * ldw + k0 + i] = __float2bfloat16_rn(v[i]);
-            else static_cast<float *>(w)[n * ldw + k0 + i] = v[i];
-        }
-    }
 }
 
+// Rows on which eight values are one aligned access.
 bool rows_aligned(const void *p, int64_t ld, int64_t esz)
 {
-    return reinterpret_cast<uintptr_t>(p) % 16 == 0 && (ld * esz) % 16 == 0;
+    return reinterpret_cast<uintptr_t>(p) % (8 * esz) == 0 && ld % 8 == 0;
+}
+
+struct PackArgs {
+    const void *w;
+    int64_t N, K, ldw;
+    int vec;
+    int64_t units;
+    uint8_t *packed;
+    int64_t ldp;
+    uint8_t *s_g;
+    int64_t lds;
+    int32_t *status;
+    unsigned blocks;
+    cudaStream_t st;
+};
+
+template <bool BF16, bool S16, int GS>
+lowbit_status pack_one(const PackArgs &a)
+{
+    return launch_pdl(gs_pack_kernel<BF16, S16, GS>, dim3(a.blocks), dim3(kThreads), 0, a.st, 0, a.w, a.N, a.K, a.ldw,
+                      a.vec, a.units, a.packed, a.ldp, a.s_g, a.lds, a.status);
+}
+
+template <bool BF16, bool S16>
+lowbit_status pack_groups(const PackArgs &a, int gshift)
+{
+    switch (gshift) {
+    case 5: return pack_one<BF16, S16, 5>(a);
+    case 6: return pack_one<BF16, S16, 6>(a);
+    case 7: return pack_one<BF16, S16, 7>(a);
+    default: return pack_one<BF16, S16, 8>(a);
+    }
 }
 
 }  // namespace
@@ -208,9 +291,10 @@ lowbit_status gs_pack_launch(const void *w, int w_bf16, int64_t N, int64_t K, in
     const int64_t units = (ldp * 2 + kUnit - 1) / kUnit;
     const int64_t blocks = (N * units + kThreads / 32 - 1) / (kThreads / 32);
     if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
-    const int vec = rows_aligned(w, ldw, w_bf16 ? 2 : 4) ? 1 : 0;
-    return launch_pdl(w_bf16 ? gs_pack_kernel<true> : gs_pack_kernel<false>, dim3(static_cast<unsigned>(blocks)),
-                      dim3(kThreads), 0, st, 0, w, N, K, ldw, vec, gshift, units, packed, ldp, s_g, s_bf16, lds, status);
+    const PackArgs a = {w, N, K, ldw, rows_aligned(w, ldw, w_bf16 ? 2 : 4) ? 1 : 0, units, packed, ldp,
+                        static_cast<uint8_t *>(s_g), lds, status, static_cast<unsigned>(blocks), st};
+    return w_bf16 ? (s_bf16 ? pack_groups<true, true>(a, gshift) : pack_groups<true, false>(a, gshift))
+                  : (s_bf16 ? pack_groups<false, true>(a, gshift) : pack_groups<false, false>(a, gshift));
 }
 
 lowbit_status gs_unpack_launch(const uint8_t *packed, int64_t ldp, const void *s_g, int s_bf16, int64_t lds, int64_t N,
@@ -218,12 +302,16 @@ lowbit_status gs_unpack_launch(const uint8_t *packed, int64_t ldp, const void *s
                                cudaStream_t st)
 {
     const int64_t words = (K + 7) / 8;
-    const int64_t blocks = (N * words + kThreads - 1) / kThreads;
+    // several words per thread once that still fills the GPU
+    const bool many = N * words >= static_cast<int64_t>(device_sm_count()) * 2048 * kInFlight;
+    const int64_t per_block = kThreads * (many ? kInFlight : 1);
+    const int64_t blocks = (N * words + per_block - 1) / per_block;
     if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
     const int vec = rows_aligned(w, ldw, w_bf16 ? 2 : 4) ? 1 : 0;
-    return launch_pdl(w_bf16 ? gs_unpack_kernel<true> : gs_unpack_kernel<false>, dim3(static_cast<unsigned>(blocks)),
-                      dim3(kThreads), 0, st, 0, packed, ldp, s_g, s_bf16, lds, N, K, gshift, words, w, ldw, vec,
-                      status);
+    auto kernel = w_bf16 ? (many ? gs_unpack_kernel<true, kInFlight> : gs_unpack_kernel<true, 1>)
+                         : (many ? gs_unpack_kernel<false, kInFlight> : gs_unpack_kernel<false, 1>);
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, 0, packed, ldp, s_g, s_bf16, lds,
+                      N, K, gshift, words, w, ldw, vec, status);
 }
 
 }  // namespace lowbit

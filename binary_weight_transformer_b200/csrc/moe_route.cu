@@ -20,6 +20,7 @@ namespace {
 // plan
 // ---------------------------------------------------------------------------
 constexpr int kPlanCtas = 8;
+constexpr int kKeys = 4;
 
 template <typename I>
 __device__ __forceinline__ int64_t load_expert(const void *experts, int64_t i)
@@ -61,27 +62,48 @@ moe_plan_kernel(const void *__restrict__ experts, int64_t slots, int E, int C, i
     const int64_t lo = (static_cast<int64_t>(rank) * warps + warp) * seg;
     const int64_t hi = lo + seg < slots ? lo + seg : slots;
     int32_t *mine = hist + warp * E;
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        int64_t e = i < hi ? load_expert<I>(experts, i) : -1;
-        if (e >= E) {
-            report(status, LOWBIT_ERR_INVALID_ARG);
-            e = -1;
+    // kKeys x 32 slots at a time: their loads are in flight together, and a
+    // segment no longer than that is read once for both passes
+    int key[kKeys];
+    auto keys = [&](int64_t i0) {
+        int64_t e[kKeys];
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            e[u] = i < hi ? load_expert<I>(experts, i) : -1;
         }
-        const int key = e < 0 ? -1 : static_cast<int>(e);
-        const uint32_t peers = __match_any_sync(0xffffffffu, key);
-        if (key >= 0 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
-        __syncwarp();
+        bool past = false;
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            past |= e[u] >= E;
+            key[u] = e[u] < 0 || e[u] >= E ? -1 : static_cast<int>(e[u]);
+        }
+        if (past) report(status, LOWBIT_ERR_INVALID_ARG);
+    };
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kKeys) {
+        keys(i0);
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            if (i0 + 32 * u >= hi) break;
+            const uint32_t peers = __match_any_sync(0xffffffffu, key[u]);
+            if (key[u] >= 0 && lane == __ffs(peers) - 1) mine[key[u]] += __popc(peers);
+            __syncwarp();
+        }
     }
     __syncthreads();
 
     const int e = threadIdx.x;
     if (e < E) {
         int32_t run = 0;
-        for (int w = 0; w < warps; ++w) {
-            const int32_t c = hist[w * E + e];
-            hist[w * E + e] = run;
-            run += c;
+        for (int w0 = 0; w0 < warps; w0 += 8) {
+            int32_t c[8];
+#pragma unroll
+            for (int w = 0; w < 8; ++w) c[w] = w0 + w < warps ? hist[(w0 + w) * E + e] : 0;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                if (w0 + w < warps) hist[(w0 + w) * E + e] = run;
+                run += c[w];
+            }
         }
         total[e] = run;
     }
@@ -89,12 +111,16 @@ moe_plan_kernel(const void *__restrict__ experts, int64_t slots, int E, int C, i
     if (C > 1) {
         tc::cluster_sync_all();
         if (e < E) {
-            for (int r = 0; r < C; ++r) {
-                int32_t c;
-                asm volatile("ld.shared::cluster.s32 %0, [%1];"
-                             : "=r"(c) : "r"(tc::map_to_peer(tc::smem_u32(total + e), static_cast<uint32_t>(r))) : "memory");
-                if (r < rank) before += c;
-                all += c;
+            int32_t c[kPlanCtas];
+#pragma unroll
+            for (int r = 0; r < kPlanCtas; ++r)
+                if (r < C)
+                    asm volatile("ld.shared::cluster.s32 %0, [%1];"
+                                 : "=r"(c[r]) : "r"(tc::map_to_peer(tc::smem_u32(total + e), static_cast<uint32_t>(r))) : "memory");
+#pragma unroll
+            for (int r = 0; r < kPlanCtas; ++r) {
+                if (r < C && r < rank) before += c[r];
+                if (r < C) all += c[r];
             }
         }
         // a block may leave only when no other still reads its counts
@@ -132,17 +158,20 @@ moe_plan_kernel(const void *__restrict__ experts, int64_t slots, int E, int C, i
     }
     __syncthreads();
 
-    for (int64_t i0 = lo; i0 < hi; i0 += 32) {
-        const int64_t i = i0 + lane;
-        const int64_t x = i < hi ? load_expert<I>(experts, i) : -1;
-        const int key = x < 0 || x >= E ? -1 : static_cast<int>(x);
-        const uint32_t peers = __match_any_sync(0xffffffffu, key);
-        int32_t p = -1;
-        if (key >= 0) p = base[key] + mine[key] + __popc(peers & ((1u << lane) - 1u));
-        __syncwarp();
-        if (key >= 0 && lane == __ffs(peers) - 1) mine[key] += __popc(peers);
-        __syncwarp();
-        if (i < hi) pos[i] = p;
+    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kKeys) {
+        if (hi - lo > 32 * kKeys) keys(i0);
+#pragma unroll
+        for (int u = 0; u < kKeys; ++u) {
+            const int64_t i = i0 + 32 * u + lane;
+            if (i - lane >= hi) break;
+            const uint32_t peers = __match_any_sync(0xffffffffu, key[u]);
+            int32_t p = -1;
+            if (key[u] >= 0) p = base[key[u]] + mine[key[u]] + __popc(peers & ((1u << lane) - 1u));
+            __syncwarp();
+            if (key[u] >= 0 && lane == __ffs(peers) - 1) mine[key[u]] += __popc(peers);
+            __syncwarp();
+            if (i < hi) pos[i] = p;
+        }
     }
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -165,15 +194,25 @@ template <> __device__ __forceinline__ uint8_t load_vec(const uint8_t *p)
     return static_cast<uint8_t>(v);
 }
 
-// The row of slot s, or -1: dropped slots are negative; a row past the end
-// (pos is device data) is reported and skipped.
-__device__ __forceinline__ int64_t slot_row(const int32_t *pos, int64_t s, int64_t rows, int32_t *status)
+// Rows of the slots s .. s + n - 1 (n <= N), or -1: dropped slots are
+// negative; a row past the end (pos is device data) is reported and skipped.
+// The loads are all issued before the first is checked.
+template <int N>
+__device__ __forceinline__ void slot_rows(const int32_t *pos, int64_t s, int n, int64_t rows, int32_t *status, int32_t (&p)[N])
 {
-    const int64_t p = static_cast<int32_t>(ld_act_u32(pos + s));
-    if (p < rows) return p;
-    report(status, LOWBIT_ERR_INVALID_ARG);
-    return -1;
+#pragma unroll
+    for (int i = 0; i < N; ++i) p[i] = i < n ? static_cast<int32_t>(ld_act_u32(pos + s + i)) : -1;
+    bool past = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (p[i] >= rows) {
+            past = true;
+            p[i] = -1;
+        }
+    if (past) report(status, LOWBIT_ERR_INVALID_ARG);
 }
+
+constexpr int kBatch = 4;  // slots taken together
 
 // A warp copies one piece (32 lanes x kVecs vectors) of a token's row to the
 // rows of its k slots.
@@ -187,7 +226,8 @@ moe_gather_kernel(const uint8_t *__restrict__ x, int64_t nvec, int64_t pieces, i
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int64_t id = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t t = id / pieces, piece = id % pieces;
+    int64_t t, piece;
+    divide(id, pieces, t, piece);
     if (t >= T) return;
     const V *src = reinterpret_cast<const V *>(x + t * ldx);
     const int64_t v0 = piece * (32 * kVecs) + lane;
@@ -196,14 +236,18 @@ moe_gather_kernel(const uint8_t *__restrict__ x, int64_t nvec, int64_t pieces, i
     for (int i = 0; i < kVecs; ++i)
         if (v0 + 32 * i < nvec) v[i] = load_vec(src + v0 + 32 * i);
     const float s = s_x != nullptr && piece == 0 ? ld_act_f32(s_x + t) : 0.0f;
-    for (int j = 0; j < k; ++j) {
-        const int64_t p = slot_row(pos, t * k + j, rows, status);
-        if (p < 0) continue;
-        V *dst = reinterpret_cast<V *>(out + p * ldo);
+    for (int j0 = 0; j0 < k; j0 += kBatch) {
+        int32_t p[kBatch];
+        slot_rows(pos, t * k + j0, k - j0, rows, status, p);
 #pragma unroll
-        for (int i = 0; i < kVecs; ++i)
-            if (v0 + 32 * i < nvec) dst[v0 + 32 * i] = v[i];
-        if (s_x != nullptr && piece == 0 && lane == 0) s_out[p] = s;
+        for (int b = 0; b < kBatch; ++b) {
+            if (p[b] < 0) continue;
+            V *dst = reinterpret_cast<V *>(out + p[b] * ldo);
+#pragma unroll
+            for (int i = 0; i < kVecs; ++i)
+                if (v0 + 32 * i < nvec) dst[v0 + 32 * i] = v[i];
+            if (s_x != nullptr && piece == 0 && lane == 0) s_out[p[b]] = s;
+        }
     }
 }
 
@@ -276,12 +320,14 @@ template <> struct Row<false, false> {
 };
 
 constexpr int kCombineVecs = 2;  // vectors per lane and row piece
-constexpr int kBatch = 4;        // slots whose loads are in flight together
 
+// A warp adds `per` consecutive pieces of a token's rows: the slots and
+// weights, which the rows' addresses wait for, are then read once for several
+// pieces.
 template <bool BF16, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 moe_combine_kernel(const void *__restrict__ ys, int64_t ldys, int64_t rows, const int32_t *__restrict__ pos,
-                   const float *__restrict__ weights, int64_t T, int k, int64_t nvec, int64_t pieces,
+                   const float *__restrict__ weights, int64_t T, int k, int64_t nvec, int64_t warps_per_row, int per,
                    void *__restrict__ y, int64_t ldy, int32_t *status)
 {
     using R = Row<BF16, VEC>;
@@ -289,42 +335,47 @@ moe_combine_kernel(const void *__restrict__ ys, int64_t ldys, int64_t rows, cons
     pdl_trigger();
     const int lane = threadIdx.x & 31;
     const int64_t id = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-    const int64_t t = id / pieces, piece = id % pieces;
+    int64_t t, part;
+    divide(id, warps_per_row, t, part);
     if (t >= T) return;
-    const int64_t v0 = piece * (32 * kCombineVecs) + lane;
-    float acc[kCombineVecs][R::kN];
+    int64_t v0 = part * (32 * kCombineVecs) * per + lane;
+    int32_t p[kBatch];
+    float w[kBatch];
+    auto slots = [&](int j0) {
 #pragma unroll
-    for (int i = 0; i < kCombineVecs; ++i)
+        for (int b = 0; b < kBatch; ++b) w[b] = weights != nullptr && j0 + b < k ? ld_act_f32(weights + t * k + j0 + b) : 1.0f;
+        slot_rows(pos, t * k + j0, k - j0, rows, status, p);
+    };
+    slots(0);
+    for (int i0 = 0; i0 < per && v0 - lane < nvec; ++i0, v0 += 32 * kCombineVecs) {
+        float acc[kCombineVecs][R::kN];
 #pragma unroll
-        for (int c = 0; c < R::kN; ++c) acc[i][c] = 0.0f;
-    for (int j0 = 0; j0 < k; j0 += kBatch) {
-        typename R::Raw raw[kBatch][kCombineVecs];
-        float w[kBatch];
-        bool on[kBatch];
+        for (int i = 0; i < kCombineVecs; ++i)
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int64_t s = t * k + j0 + b;
-            const int64_t p = j0 + b < k ? slot_row(pos, s, rows, status) : -1;
-            on[b] = p >= 0;
-            w[b] = on[b] && weights != nullptr ? ld_act_f32(weights + s) : 1.0f;
+            for (int c = 0; c < R::kN; ++c) acc[i][c] = 0.0f;
+        for (int j0 = 0; j0 < k; j0 += kBatch) {
+            if (k > kBatch && (j0 != 0 || i0 != 0)) slots(j0);
+            typename R::Raw raw[kBatch][kCombineVecs];
 #pragma unroll
-            for (int i = 0; i < kCombineVecs; ++i)
-                if (on[b] && v0 + 32 * i < nvec) raw[b][i] = R::load(ys, p * ldys + (v0 + 32 * i) * R::kN);
+            for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+                for (int i = 0; i < kCombineVecs; ++i)
+                    if (p[b] >= 0 && v0 + 32 * i < nvec) raw[b][i] = R::load(ys, p[b] * ldys + (v0 + 32 * i) * R::kN);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (p[b] < 0) continue;
+#pragma unroll
+                for (int i = 0; i < kCombineVecs; ++i)
+                    if (v0 + 32 * i < nvec) {
+#pragma unroll
+                        for (int c = 0; c < R::kN; ++c) acc[i][c] = __fmaf_rn(w[b], R::get(raw[b][i], c), acc[i][c]);
+                    }
+            }
         }
 #pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            if (!on[b]) continue;
-#pragma unroll
-            for (int i = 0; i < kCombineVecs; ++i)
-                if (v0 + 32 * i < nvec) {
-#pragma unroll
-                    for (int c = 0; c < R::kN; ++c) acc[i][c] = __fmaf_rn(w[b], R::get(raw[b][i], c), acc[i][c]);
-                }
-        }
+        for (int i = 0; i < kCombineVecs; ++i)
+            if (v0 + 32 * i < nvec) R::store(y, t * ldy + (v0 + 32 * i) * R::kN, acc[i]);
     }
-#pragma unroll
-    for (int i = 0; i < kCombineVecs; ++i)
-        if (v0 + 32 * i < nvec) R::store(y, t * ldy + (v0 + 32 * i) * R::kN, acc[i]);
 }
 
 // W warps of a block share a token (kWarps / W tokens per block): each takes
@@ -347,14 +398,13 @@ moe_combine_backward_kernel(const void *__restrict__ dy, int64_t lddy, const voi
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kWarps / W) + warp / W;
     for (int j0 = 0; j0 < k; j0 += kBatch) {
         float dot[kBatch], w[kBatch];
-        int64_t p[kBatch];
+        int32_t p[kBatch];
 #pragma unroll
         for (int b = 0; b < kBatch; ++b) {
-            const int64_t s = t * k + j0 + b;
             dot[b] = 0.0f;
-            p[b] = t < T && j0 + b < k ? slot_row(pos, s, rows, status) : -1;
-            w[b] = p[b] >= 0 ? ld_act_f32(weights + s) : 0.0f;
+            w[b] = t < T && j0 + b < k ? ld_act_f32(weights + t * k + j0 + b) : 0.0f;
         }
+        slot_rows(pos, t * k + j0, t < T ? k - j0 : 0, rows, status, p);
         if (t < T) {
             for (int64_t v = lane + 32 * wt; v < nvec; v += 32 * W) {
                 const typename R::Raw g = R::load(dy, t * lddy + v * R::kN);
@@ -461,12 +511,18 @@ lowbit_status moe_combine_launch(const void *ys, int bf16, int64_t ldys, int64_t
     const bool vec = multiple_of(16, ys, ldys * esz, y, ldy * esz, K * esz);
     const int64_t nvec = vec ? K * esz / 16 : K;
     const int64_t pieces = (nvec + 32 * kCombineVecs - 1) / (32 * kCombineVecs);
-    const int64_t blocks = (T * pieces + kWarps - 1) / kWarps;
+    // Pieces per warp: as many as leave about 32 warps for every SM.
+    int64_t per = T * pieces / (static_cast<int64_t>(device_sm_count()) * 32);
+    if (per > pieces) per = pieces;
+    if (per < 1) per = 1;
+    if (per > 64) per = 64;
+    const int64_t warps = (pieces + per - 1) / per;
+    const int64_t blocks = (T * warps + kWarps - 1) / kWarps;
     if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
     auto kernel = bf16 ? (vec ? moe_combine_kernel<true, true> : moe_combine_kernel<true, false>)
                        : (vec ? moe_combine_kernel<false, true> : moe_combine_kernel<false, false>);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, 0, ys, ldys, rows, pos,
-                      weights, T, k, nvec, pieces, y, ldy, status);
+                      weights, T, k, nvec, warps, static_cast<int>(per), y, ldy, status);
 }
 
 lowbit_status moe_combine_backward_launch(const void *dy, int64_t lddy, const void *ys, int64_t ldys, int bf16,
