@@ -61,6 +61,7 @@ lowbit_status check_slots(const void *pos, int64_t T, int k, int64_t rows)
 lowbit_status gs_product(const GsArgs &a, cudaStream_t st)
 {
     const int64_t rows = a.offsets != nullptr ? a.M / a.E : a.M;
+    if (gs_gemv_takes(a)) return gs_gemv_launch(a, st);
     return rows <= 64 ? gs_mma_launch(a, st) : gs_gemm_launch(a, st);
 }
 

@@ -1,0 +1,187 @@
+// gs_gemv.cu -- the group-scaled 4-bit product for one token, on dp4a.
+//
+//   y[n] = s_x * sum_g s_g[n,g] * (sum_{k in g} q[k] c[n,k])
+//
+// A lane takes 16-byte chunks of a weight row: 32 consecutive codes, which
+// always lie in one group (groups are multiples of 32 codes), so a chunk is
+// eight dp4a on codes expanded in registers, one conversion and one
+// multiply-add with the chunk's scale -- about 35 instructions per 1024 codes,
+// against 90 for the tensor-core kernel, whose smallest tile is eight tokens.
+// (From two tokens on that one wins: 9728 -> 2560 with four takes 11 us there
+// and 15 us as dp4a.)  Decode is bound by latency: a warp has R rows of kAhead
+// chunks per lane and their scales on their way at once, which for most rows
+// is all it will read, and the token's codes are staged in shared memory
+// meanwhile.  The warps of a block that share rows take a range of K each.
+#include "gs_internal.cuh"
+#include "tc_common.cuh"
+
+namespace lowbit {
+namespace gsv {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int64_t kMaxCodes = 96 * 1024;  // staged token codes
+
+template <int R> __host__ __device__ constexpr int ahead() { return R == 4 ? 3 : 5; }
+// Resident blocks per SM that the registers are limited for.
+template <int R> __host__ __device__ constexpr int resident() { return R == 4 ? 2 : 3; }
+
+// R: weight rows per warp.
+template <int R>
+__global__ void __launch_bounds__(kThreads, resident<R>())
+gs_gemv_kernel(const GsArgs a, int chunks, int kwarps)
+{
+    constexpr int kAhead = ahead<R>();
+    extern __shared__ __align__(16) uint8_t smem[];  // codes: [half of a chunk][chunk] 16 bytes
+    __shared__ float sums[kWarps][R];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kw = warp % kwarps;
+    const int n0 = (static_cast<int>(blockIdx.x) * (kWarps / kwarps) + warp / kwarps) * R;
+    const int per = (chunks + kwarps - 1) / kwarps;
+    const int c_lo = kw * per, c_hi = c_lo + per < chunks ? c_lo + per : chunks;
+    const uint32_t q_base = tc::smem_u32(smem);
+
+    if (a.prefetch == 0) pdl_wait();
+    pdl_trigger();
+    const int s_shift = a.s_bf16 ? 1 : 2;
+    const uint8_t *row[R], *srow[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const int n = n0 + r < a.N ? n0 + r : 0;
+        row[r] = a.packed + n * a.ldp;
+        srow[r] = static_cast<const uint8_t *>(a.s_g) + ((n * a.lds) << s_shift);
+    }
+    uint4 w[R][kAhead];
+    uint32_t sb[R][kAhead];
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int c = c0 + lane + 32 * i;
+#pragma unroll
+            for (int r = 0; r < R; ++r)
+                w[r][i] = c < c_hi && n0 + r < a.N ? ld_stream_u4(row[r] + static_cast<int64_t>(c) * 16)
+                                                   : make_uint4(0, 0, 0, 0);
+        }
+        // the bits of the scales: converting them here would wait for each
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int c = c0 + lane + 32 * i;
+            const int64_t at = (c << 5 >> a.gshift) << s_shift;
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                sb[r][i] = 0;
+                if (c < c_hi) {
+                    if (a.s_bf16) {
+                        uint16_t h;
+                        asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(h) : "l"(srow[r] + at));
+                        sb[r][i] = h;
+                    } else {
+                        asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(sb[r][i]) : "l"(srow[r] + at));
+                    }
+                }
+            }
+        }
+    };
+    fetch(c_lo);
+    if (a.prefetch != 0) pdl_wait();
+    // the token's codes, zeros past K
+    for (int p = threadIdx.x; p < 2 * chunks; p += kThreads) {
+        const int left = static_cast<int>(a.K) - p * 16;
+        const int valid = left >= 16 ? 16 : left > 0 ? left : 0;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                     ::"r"(q_base + static_cast<uint32_t>(((p & 1) * chunks + (p >> 1)) * 16)),
+                       "l"(a.q + (valid > 0 ? p * 16 : 0)), "r"(valid) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const float sx = __fmul_rn(ld_act_f32(a.s_x), 0.0625f);  // the factor 16 of the shifted codes leaves here
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+
+    float acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = 0.0f;
+    for (int c0 = c_lo;;) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int c = c0 + lane + 32 * i;
+            if (c < c_hi) {
+                const uint4 q0 = tc::lds128(q_base + static_cast<uint32_t>(c * 16));
+                const uint4 q1 = tc::lds128(q_base + static_cast<uint32_t>((chunks + c) * 16));
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const uint4 x = w[r][i];
+                    int d = 0;  // word j of the chunk: codes 8j .. 8j + 7, four in the low nibbles, four in the high
+                    d = __dp4a(static_cast<int>(i4_expand(x.x, 0)), static_cast<int>(q0.x), d);
+                    d = __dp4a(static_cast<int>(i4_expand(x.x, 1)), static_cast<int>(q0.y), d);
+                    d = __dp4a(static_cast<int>(i4_expand(x.y, 0)), static_cast<int>(q0.z), d);
+                    d = __dp4a(static_cast<int>(i4_expand(x.y, 1)), static_cast<int>(q0.w), d);
+                    d = __dp4a(static_cast<int>(i4_expand(x.z, 0)), static_cast<int>(q1.x), d);
+                    d = __dp4a(static_cast<int>(i4_expand(x.z, 1)), static_cast<int>(q1.y), d);
+                    d = __dp4a(static_cast<int>(i4_expand(x.w, 0)), static_cast<int>(q1.z), d);
+                    d = __dp4a(static_cast<int>(i4_expand(x.w, 1)), static_cast<int>(q1.w), d);
+                    acc[r] = __fmaf_rn(__uint_as_float(a.s_bf16 ? sb[r][i] << 16 : sb[r][i]), __int2float_rn(d), acc[r]);
+                }
+            }
+        }
+        c0 += 32 * kAhead;
+        if (c0 >= c_hi) break;
+        fetch(c0);
+    }
+
+    float v = 0.0f;  // lane r: the sum of row r
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) acc[r] += __shfl_xor_sync(0xffffffffu, acc[r], o);
+        if (lane == r) v = acc[r];
+    }
+    if (kwarps > 1) {
+        if (lane < R) sums[warp][lane] = v;
+        __syncthreads();
+        if (kw == 0 && lane < R)
+            for (int p = 1; p < kwarps; ++p) v += sums[warp + p][lane];
+    }
+    if (kw == 0 && lane < R && n0 + lane < a.N) {
+        const float f = __fmul_rn(v, sx);
+        if (a.y_bf16) static_cast<__nv_bfloat16 *>(a.y)[n0 + lane] = __float2bfloat16_rn(f);
+        else static_cast<float *>(a.y)[n0 + lane] = f;
+    }
+}
+
+template <int R>
+lowbit_status launch(const GsArgs &a, int64_t kwarps, cudaStream_t st)
+{
+    const int64_t chunks = (a.K + 31) / 32;
+    const int64_t rows = kWarps / kwarps * R;
+    static PerDevice configured;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
+    if (configured.get(dev, [&] {
+            return cudaFuncSetAttribute(gs_gemv_kernel<R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(kMaxCodes)) == cudaSuccess ? 1 : 0;
+        }) <= 0)
+        return LOWBIT_ERR_CUDA;
+    return launch_pdl(gs_gemv_kernel<R>, dim3(static_cast<unsigned>((a.N + rows - 1) / rows)), dim3(kThreads),
+                      static_cast<size_t>(chunks) * 32, st, 0, a, static_cast<int>(chunks), static_cast<int>(kwarps));
+}
+
+}  // namespace gsv
+
+bool gs_gemv_takes(const GsArgs &a) { return a.offsets == nullptr && a.M == 1 && (a.K + 31) / 32 * 32 <= gsv::kMaxCodes; }
+
+lowbit_status gs_gemv_launch(const GsArgs &a, cudaStream_t st)
+{
+    const int64_t sms = device_sm_count();
+    const int64_t chunks = (a.K + 31) / 32;
+    // Four rows per warp share their codes' loads and the fixed part, where
+    // two rows would take more warps than are resident at once (a second wave
+    // of blocks costs 3 us); else two, with K split while the warps fit and a
+    // range is more than one load.
+    const int64_t fit = sms * gsv::resident<2>() * gsv::kWarps * 2;  // rows
+    if (a.N > fit) return gsv::launch<4>(a, 1, st);
+    int64_t kwarps = 1;
+    while (kwarps < gsv::kWarps && a.N * kwarps * 2 <= fit && chunks > 32 * kwarps) kwarps *= 2;
+    return gsv::launch<2>(a, kwarps, st);
+}
+
+}  // namespace lowbit

@@ -75,6 +75,9 @@ __device__ __forceinline__ void divide(int64_t id, int64_t d, int64_t &quotient,
     }
 }
 
+// One token whose codes fit the shared memory of gs_gemv_launch.
+bool gs_gemv_takes(const GsArgs &a);
+lowbit_status gs_gemv_launch(const GsArgs &a, cudaStream_t st);
 lowbit_status gs_mma_launch(const GsArgs &a, cudaStream_t st);
 lowbit_status gs_gemm_launch(const GsArgs &a, cudaStream_t st);
 lowbit_status gs_pack_launch(const void *w, int w_bf16, int64_t N, int64_t K, int64_t ldw, int gshift, uint8_t *packed,
