@@ -176,6 +176,28 @@ __device__ __forceinline__ void expand(uint32_t P, uint32_t E, int et)
     }
 }
 
+// 16 columns of this thread's lane: the load, and the wait for all of the
+// thread's loads (its registers are operands, so no use of them moves above).
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_wait16(uint32_t (&v)[16])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]),
+                   "+r"(v[15])
+                 :
+                 : "memory");
+}
+
 // The group scales of one weight row.
 template <bool SB>
 struct ScaleRow {
@@ -285,8 +307,8 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
 {
     constexpr int ST = stages<NT>(), SE = kExpStages;
     constexpr int Q_BYTES = q_bytes<NT>();
-    constexpr int SUB = NT / 2;                  // tokens of a half: of one MMA and of a drain warp
-    constexpr int QR = SUB / 2;                  // tokens of a half that each CTA stages
+    constexpr int SUB = NT / 2;                  // tokens that a CTA stages, and that a drain warp owns
+    constexpr int NB = 512 / NT;                 // accumulators
     constexpr int FPB = PER >= 4 ? 1 : 4 / PER;  // groups that end in a K block (PER = 8: in every other one)
     static_assert(SE < ST, "an expansion stage is freed through the MMA barrier of an older TMA stage");
 
@@ -299,11 +321,11 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     uint8_t *sStage = reinterpret_cast<uint8_t *>(sX + kDrainWarps * SUB);  // output staging, per drain warp
     uint64_t *bars = reinterpret_cast<uint64_t *>(sStage + kDrainWarps * kStageBytes);
     uint64_t *full_tma = bars;                   // a stage's tiles have landed
-    uint64_t *mma_done = bars + ST;              // both halves' MMAs on the stage are complete
+    uint64_t *mma_done = bars + ST;              // the stage's MMAs are complete
     uint64_t *full_exp = bars + 2 * ST;          // both CTAs have expanded the stage (even CTA's is used)
-    uint64_t *acc_full = full_exp + SE;          // [half][b]: a group's sums are in accumulator b of a half
-    uint64_t *acc_empty = acc_full + 4;          // [half][b]: both CTAs have drained it (even CTA's is used)
-    uint64_t *drain = acc_full + 8;              // [half]
+    uint64_t *acc_full = full_exp + SE;          // a group's sums are in accumulator b
+    uint64_t *acc_empty = acc_full + 4;          // both CTAs have drained it (even CTA's is used)
+    uint64_t *drain = acc_full + 8;
     volatile uint32_t *tmem_slot = reinterpret_cast<volatile uint32_t *>(acc_full + 10);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(acc_full + 11);
     Plan *plan = reinterpret_cast<Plan *>(acc_full + 12);
@@ -315,14 +337,14 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(&full_tma[s], 1);
-            mbar_init(&mma_done[s], 2);
+            mbar_init(&mma_done[s], 1);
         }
         for (int s = 0; s < SE; ++s) mbar_init(&full_exp[s], 8);
-        for (int b = 0; b < 4; ++b) {
+        for (int b = 0; b < NB; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], kDrainWarps);
+            mbar_init(&acc_empty[b], 2 * kDrainWarps);
         }
-        for (int x = 0; x < 2; ++x) mbar_init(&drain[x], 1);
+        mbar_init(drain, 1);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&map_q)) : "memory");
@@ -377,14 +399,13 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 uint32_t g = 0;
                 bool ok = true;
                 while (ok && tiles.next(tl)) {
-                    const int t0 = tl.row0 + static_cast<int>(rank) * QR;
+                    const int t0 = tl.row0 + static_cast<int>(rank) * SUB;
                     const int w0 = tl.w0 + static_cast<int>(rank) * kRows;
                     for (int kb = 0; kb < nkb; ++kb, ++g) {
                         const int s = g % ST;
                         if (!wait_bar(&mma_done[s], ((g / ST) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
                         mbar_arrive_expect_tx(&full_tma[s], Q_BYTES + P_BYTES);
                         tma_load_2d(sQ + s * Q_BYTES, &map_q, &full_tma[s], kb * BK, t0);
-                        tma_load_2d(sQ + s * Q_BYTES + QR * BK, &map_q, &full_tma[s], kb * BK, t0 + SUB);
                         tma_load_3d(sP + s * P_BYTES, &map_p, &full_tma[s], kb * (BK / 2), w0, tl.e);
                     }
                 }
@@ -395,12 +416,10 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                     }
                 }
             }
-        } else if (warp < 3) {
-            // ---------------- MMA issuers (even CTA): one half of the tokens each ----------------
+        } else if (warp == 1) {
+            // ---------------- MMA issuer (even CTA) ----------------
             if (leader && lane == 0) {
-                const int x = warp - 1;
-                // rows x * QR .. of each CTA's token tile are this half
-                const uint64_t qdesc0 = sw128_desc(smem_u32(sQ) + static_cast<uint32_t>(x * QR * BK));
+                const uint64_t qdesc0 = sw128_desc(smem_u32(sQ));
                 const uint64_t edesc0 = sw128_desc(smem_u32(sE));
                 Tiles<NT> tiles(plan, a);
                 Tile tl;
@@ -419,19 +438,19 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         const bool closes = PER <= 4 || (kb & 1) != 0 || kb + 1 == nkb;
 #pragma unroll
                         for (int f = 0; f < FPB; ++f) {
-                            const int b = 2 * x + (h & 1);
+                            const int b = h % NB;
                             // both polls before either result is needed
-                            const uint32_t ph_acc = ((h >> 1) & 1u) ^ 1u, ph_exp = (g / SE) & 1u;
+                            const uint32_t ph_acc = ((h / NB) & 1u) ^ 1u, ph_exp = (g / SE) & 1u;
                             const bool acc_on = !opens || mbar_try_wait(&acc_empty[b], ph_acc);
                             const bool exp_on = f != 0 || mbar_try_wait(&full_exp[s2], ph_exp);
                             if (!acc_on && !wait_bar(&acc_empty[b], ph_acc, abort_flag, a.status)) { ok = false; break; }
                             if (!exp_on && !wait_bar(&full_exp[s2], ph_exp, abort_flag, a.status)) { ok = false; break; }
                             tc_fence_after();
-                            const uint32_t d = tmem_base + static_cast<uint32_t>(b * SUB);
+                            const uint32_t d = tmem_base + static_cast<uint32_t>(b * NT);
 #pragma unroll
                             for (int kk = f * 4 / FPB; kk < (f + 1) * 4 / FPB; ++kk)
                                 mma_i8_pair(d, edesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)),
-                                            qdesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)), idesc<SUB>(),
+                                            qdesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)), idesc<NT>(),
                                             kk == f * 4 / FPB && opens ? 0u : 1u);
                             if (closes) {
                                 commit_both(&acc_full[b]);
@@ -441,8 +460,8 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         if (ok) commit_both(&mma_done[s1]);
                     }
                 }
-                commit_self(&drain[x]);
-                drain_bar(&drain[x], 0);
+                commit_self(drain);
+                drain_bar(drain, 0);
             }
         } else if (warp >= 4) {
             // ---------------- expanders: own 128 weight rows ----------------
@@ -473,8 +492,8 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
         const int quarter = warp & 3, x = (warp - 8) >> 2;
         float *sx = sX + (warp - 8) * SUB;
-        const uint32_t empty_leader = map_to_peer(smem_u32(acc_empty + 2 * x), 0);
-        const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(2 * x * SUB);
+        const uint32_t empty_leader = map_to_peer(smem_u32(acc_empty), 0);
+        const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(x * SUB);
         const int groups = static_cast<int>((a.K - 1) >> a.gshift) + 1;
         const int ends = PER == 8 ? (nkb + 1) / 2 : nkb * FPB;  // groups of the whole K blocks
         const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy % (a.y_bf16 ? 8 : 4) == 0;
@@ -482,56 +501,78 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         Tile tl;
         uint32_t h = 0;  // groups so far
         bool ok = true;
-        while (ok && tiles.next(tl)) {
+        while (tiles.next(tl)) {
             const int n = tl.w0 + static_cast<int>(rank) * kRows + quarter * 32 + lane;
             const bool row_on = n < a.N;
             const ScaleRow<SB> scales(a.s_g, tl.e * a.sstride + static_cast<int64_t>(row_on ? n : 0) * a.lds);
             const int row0 = tl.row0 + x * SUB;  // this warp's first token
             const int left = tl.hi - row0;
-            // the factor 16 of the shifted codes leaves with the token scale
+            float s_next = scales.at(0);
+            float xr[SUB / 32];  // token scales, needed (in shared memory) when the tile is stored
 #pragma unroll
-            for (int i = lane; i < SUB; i += 32) sx[i] = i < left ? __fmul_rn(ld_act_f32(a.s_x + row0 + i), 0.0625f) : 0.0f;
-            __syncwarp();
+            for (int i = 0; i < SUB / 32; ++i) xr[i] = lane + 32 * i < left ? ld_act_f32(a.s_x + row0 + lane + 32 * i) : 0.0f;
             float2 acc[SUB / 2];
 #pragma unroll
             for (int j = 0; j < SUB / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
-            float s_next = scales.at(0);
-            bool polled = mbar_try_wait(&acc_full[2 * x + (h & 1)], (h >> 1) & 1u);
+            // One sequence of 16-column chunks over all groups: while a chunk
+            // is multiplied, the next one, of the next group too, is on its
+            // way.  What a group costs beside its multiply-adds (poll, fence,
+            // first load: about 600 cycles when they came one after the other)
+            // is hidden by that.  A load is issued and waited for in the same
+            // straight piece of code, so its registers are never copied while
+            // it is in flight.
+            constexpr int CH = 16, NCH = SUB / CH;
+            static_assert(NCH % 2 == 0, "a group's first chunk goes to v[0]");
+            uint32_t v[2][CH];
+            auto wait_full = [&](uint32_t hh) {
+                int ready = 0;
+                if (lane == 0) ready = wait_bar(&acc_full[hh % NB], (hh / NB) & 1u, abort_flag, a.status) ? 1 : 0;
+                return __shfl_sync(0xffffffffu, ready, 0) != 0;
+            };
+            ok = wait_full(h);
+            if (!ok) break;
+            tc_fence_after();
+            tmem_ld16(tacc + (h % NB) * NT, v[0]);
+            tmem_wait16(v[0]);
             for (int gr = 0; gr < ends; ++gr, ++h) {
-                const uint32_t b = h & 1;
+                const uint32_t b = h % NB, bn = (h + 1) % NB;
+                const bool more = gr + 1 < ends;
                 const float s = s_next;
                 s_next = scales.at(gr + 1 < groups ? gr + 1 : 0);
-                // polled by the whole warp during the previous group's
-                // multiply-adds; usually complete
-                if (!__all_sync(0xffffffffu, polled)) {
-                    int ready = 0;
-                    if (lane == 0) ready = wait_bar(&acc_full[2 * x + b], (h >> 1) & 1u, abort_flag, a.status) ? 1 : 0;
-                    ok = __shfl_sync(0xffffffffu, ready, 0) != 0;
-                    if (!ok) break;
-                }
-                tc_fence_after();
-                const uint32_t col = tacc + b * SUB;
-                uint32_t v[2][32];
-                tmem_ld_32cols_async(col, v[0]);
+                bool polled = true;
 #pragma unroll
-                for (int c = 0; c < SUB / 32; ++c) {
-                    tmem_ld_wait(v[c & 1]);
-                    if (c + 1 < SUB / 32) {
-                        // the next columns arrive during these columns' multiply-adds
-                        tmem_ld_32cols_async(col + static_cast<uint32_t>((c + 1) * 32), v[(c + 1) & 1]);
-                    } else {
-                        // the sums are in registers: the next group may use the buffer
+                for (int c = 0; c < NCH; ++c) {
+                    uint32_t next = tacc + b * NT + static_cast<uint32_t>((c + 1) * CH);
+                    if (c == NCH - 2 && more) polled = mbar_try_wait(&acc_full[bn], ((h + 1) / NB) & 1u);
+                    if (c == NCH - 1) {
+                        if (more) {
+                            if (!__all_sync(0xffffffffu, polled)) ok = wait_full(h + 1);
+                            tc_fence_after();
+                        }
+                        // (after the tile's last group, and when a wait gave
+                        // up, these columns are read and not used)
+                        next = tacc + (more ? bn : b) * NT;
+                    }
+                    tmem_ld16(next, v[(c + 1) & 1]);
+                    // groups past the row's last hold zero sums
+#pragma unroll
+                    for (int j = 0; j < CH / 2; ++j) fma2(acc[CH / 2 * c + j], s, v[c & 1][2 * j], v[c & 1][2 * j + 1]);
+                    tmem_wait16(v[(c + 1) & 1]);
+                    if (c == NCH - 2) {
+                        // the group's sums are in registers: the next group may use the buffer
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_remote(empty_leader + b * 8);
-                        polled = mbar_try_wait(&acc_full[2 * x + (b ^ 1)], ((h + 1) >> 1) & 1u);
                     }
-                    // groups past the row's last hold zero sums
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) fma2(acc[16 * c + j], s, v[c & 1][2 * j], v[c & 1][2 * j + 1]);
                 }
+                if (!ok) break;
             }
-            if (ok) {
+            if (!ok) break;
+            {
+                // the factor 16 of the shifted codes leaves with the token scale
+#pragma unroll
+                for (int i = 0; i < SUB / 32; ++i) sx[lane + 32 * i] = __fmul_rn(xr[i], 0.0625f);
+                __syncwarp();
                 const uint32_t stage = smem_u32(sStage) + static_cast<uint32_t>((warp - 8) * kStageBytes);
                 if (a.y_bf16)
                     store_columns<__nv_bfloat16, SUB>(a.y, a.ldy, row0, n - lane, a.N, left, vec, smem_u32(sx), stage, lane, acc);
@@ -602,7 +643,7 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
     if (resident <= 0) return LOWBIT_ERR_CUDA;
     CUtensorMap mq, mp;
     if (!make_map_2d(&mq, a.q, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M), static_cast<uint64_t>(a.ldq), BK,
-                     NT / 4, CU_TENSOR_MAP_SWIZZLE_128B) ||
+                     NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_weight_map(&mp, a))
         return LOWBIT_ERR_CUDA;
     // experts: their row counts are on the device; at most this many token tiles
