@@ -245,47 +245,80 @@ __device__ __forceinline__ void store_elements(T *p, int64_t ldy, int left, uint
 }
 
 // The same through shared memory, 16 tokens at a time, as 16-byte stores of
-// whole token rows: 512 bytes per instruction.  The element stores took 5000
-// cycles per tile of 256 x 256, which nothing overlaps.
-template <typename T, int NC>
-__device__ __forceinline__ void store_staged(T *p, int64_t ldy, int left, uint32_t sx, uint32_t stage, int lane,
+// whole token rows: 512 bytes per instruction.
+//
+// bf16: a lane packs its 16 tokens (two 16-byte stores), and ldmatrix.trans
+// turns 8 tokens x 32 rows at a time: the row addresses given to matrix i are
+// weight rows 8 (r / 2) + 2 i + r % 2, so lane T receives rows 8 (T % 4) .. + 7
+// of token T / 4 in its four registers, one 16-byte store.  Staged rows are 48
+// bytes apart, and 32 more every 8 rows, which keeps both sides free of bank
+// conflicts.  (With one 2-byte store per value this took 5500 cycles for a tile
+// of 256 x 256, which nothing overlaps.)
+template <int NC>
+__device__ __forceinline__ void store_staged(__nv_bfloat16 *p, int64_t ldy, int left, uint32_t sx, uint32_t stage, int lane,
                                              const float2 (&acc)[NC / 2])
 {
-    constexpr int kRow = 32 * sizeof(T) + 16;             // bytes of a staged token
-    constexpr int kPieces = 32 * sizeof(T) / 16;          // 16-byte pieces of it
-    constexpr int kPer = 32 / kPieces;                    // tokens per store instruction
-    const uint32_t mine = stage + static_cast<uint32_t>(lane * sizeof(T));
-    const uint32_t from = stage + static_cast<uint32_t>(lane / kPieces * kRow + lane % kPieces * 16);
-    char *dst = reinterpret_cast<char *>(p + lane / kPieces * ldy) + lane % kPieces * 16;
+    const uint32_t mine = stage + static_cast<uint32_t>(lane * 48 + (lane >> 3) * 32);
+    const int r = lane & 7, from_row = 8 * (r >> 1) + 2 * (lane >> 3) + (r & 1);
+    const uint32_t from = stage + static_cast<uint32_t>(from_row * 48 + (from_row >> 3) * 32);
+    __nv_bfloat16 *dst = p + (lane >> 2) * ldy + 8 * (lane & 3);
+    left -= lane >> 2;
 #pragma unroll
     for (int j0 = 0; j0 < NC; j0 += kStageTokens) {
-        if (j0 >= left) break;
+        uint4 xs[kStageTokens / 4];
+#pragma unroll
+        for (int j = 0; j < kStageTokens / 4; ++j) xs[j] = lds128(sx + j0 * 4 + j * 16);
+        uint32_t w[kStageTokens / 2];
+#pragma unroll
+        for (int j = 0; j < kStageTokens / 2; ++j) {
+            const float2 a = acc[j0 / 2 + j];
+            const uint4 x = xs[j / 2];
+            const __nv_bfloat162 b = __floats2bfloat162_rn(__fmul_rn(a.x, __uint_as_float(j & 1 ? x.z : x.x)),
+                                                           __fmul_rn(a.y, __uint_as_float(j & 1 ? x.w : x.y)));
+            w[j] = *reinterpret_cast<const uint32_t *>(&b);
+        }
+        sts128(mine, make_uint4(w[0], w[1], w[2], w[3]));
+        sts128(mine + 16, make_uint4(w[4], w[5], w[6], w[7]));
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint4 v;
+            asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(from + h * 16) : "memory");
+            if (j0 + 8 * h < left) *reinterpret_cast<uint4 *>(dst) = v;
+            dst += 8 * ldy;
+        }
+        __syncwarp();
+    }
+}
+
+// fp32: one 4-byte store per value, whole rows read back.
+template <int NC>
+__device__ __forceinline__ void store_staged(float *p, int64_t ldy, int left, uint32_t sx, uint32_t stage, int lane,
+                                             const float2 (&acc)[NC / 2])
+{
+    constexpr int kRow = 32 * 4 + 16;  // bytes of a staged token
+    const uint32_t mine = stage + static_cast<uint32_t>(lane * 4);
+    const uint32_t from = stage + static_cast<uint32_t>((lane >> 3) * kRow + (lane & 7) * 16);
+    float *dst = p + (lane >> 3) * ldy + (lane & 7) * 4;
+    left -= lane >> 3;
+#pragma unroll
+    for (int j0 = 0; j0 < NC; j0 += kStageTokens) {
         uint4 xs[kStageTokens / 4];
 #pragma unroll
         for (int j = 0; j < kStageTokens / 4; ++j) xs[j] = lds128(sx + j0 * 4 + j * 16);
 #pragma unroll
-        for (int j = 0; j < kStageTokens; j += 4) {
-            const uint4 x = xs[j / 4];
-            const float2 a0 = acc[(j0 + j) / 2], a1 = acc[(j0 + j) / 2 + 1];
-            const float f[4] = {__fmul_rn(a0.x, __uint_as_float(x.x)), __fmul_rn(a0.y, __uint_as_float(x.y)),
-                                __fmul_rn(a1.x, __uint_as_float(x.z)), __fmul_rn(a1.y, __uint_as_float(x.w))};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (sizeof(T) == 2) {
-                    const __nv_bfloat16 b = __float2bfloat16_rn(f[i]);
-                    asm volatile("st.shared.b16 [%0], %1;" ::"r"(mine + (j + i) * kRow),
-                                 "h"(*reinterpret_cast<const uint16_t *>(&b)) : "memory");
-                } else {
-                    asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + (j + i) * kRow), "f"(f[i]) : "memory");
-                }
-            }
+        for (int j = 0; j < kStageTokens; ++j) {
+            const float2 a = acc[(j0 + j) / 2];
+            const float f = __fmul_rn(j & 1 ? a.y : a.x, __uint_as_float((&xs[j / 4].x)[j & 3]));
+            asm volatile("st.shared.f32 [%0], %1;" ::"r"(mine + j * kRow), "f"(f) : "memory");
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kStageTokens / kPer; ++i) {
-            const uint4 v = lds128(from + i * kPer * kRow);
-            if (j0 + i * kPer + lane / kPieces < left) *reinterpret_cast<uint4 *>(dst) = v;
-            dst += kPer * ldy * static_cast<int64_t>(sizeof(T));
+        for (int i = 0; i < kStageTokens / 4; ++i) {
+            const uint4 v = lds128(from + i * 4 * kRow);
+            if (j0 + i * 4 < left) *reinterpret_cast<uint4 *>(dst) = v;
+            dst += 4 * ldy;
         }
         __syncwarp();
     }
@@ -296,7 +329,7 @@ __device__ __forceinline__ void store_columns(void *y, int64_t ldy, int64_t row0
                                               uint32_t sx, uint32_t stage, int lane, const float2 (&acc)[NC / 2])
 {
     T *p = static_cast<T *>(y) + row0 * ldy + n0;
-    if (vec && n0 + 32 <= N) store_staged<T, NC>(p, ldy, left, sx, stage, lane, acc);
+    if (vec && n0 + 32 <= N) store_staged<NC>(p, ldy, left, sx, stage, lane, acc);
     else if (n0 + lane < N) store_elements<T, NC>(p + lane, ldy, left, sx, acc);
 }
 
