@@ -442,11 +442,11 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         tma_load_3d(sP + s * P_BYTES, &map_p, &full_tma[s], kb * (BK / 2), w0, tl.e);
                     }
                 }
-                if (!ok) {
-                    for (uint32_t i = 0; i < ST && i < g; ++i) {
-                        const uint32_t gi = g - 1 - i;
-                        drain_bar(&full_tma[gi % ST], (gi / ST) & 1u);
-                    }
+                // every copy issued lands before the block leaves, also when
+                // the other roles gave up on a wait
+                for (uint32_t i = 0; i < ST && i < g; ++i) {
+                    const uint32_t gi = g - 1 - i;
+                    drain_bar(&full_tma[gi % ST], (gi / ST) & 1u);
                 }
             }
         } else if (warp == 1) {

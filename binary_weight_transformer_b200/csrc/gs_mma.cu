@@ -7,7 +7,8 @@
 // enter the integer sum as c << 4 (expanding a nibble to the top of its byte
 // makes the sign free) and the factor 16 leaves in the last multiply, exactly.
 //
-// A = 16 tokens x 32 codes, B = 32 codes x 8 weight rows, C = 16 x 8.  The 32
+// A = 16 tokens x 32 codes, B = 32 codes x 8 weight rows, C = 16 x 8 (or half of
+// A and C with up to 8 tokens).  The 32
 // positions of a K step may be any 32 codes as long as A and B agree, so lane
 // (g, t) of a warp loads ONE 16-byte piece of weight row g -- 32 consecutive
 // codes, piece t of a unit of 128 -- and uses its words as the B fragments of
@@ -17,7 +18,7 @@
 // a step may only hold codes of one group: the four lanes of a row exchange
 // words (2 or 4 shuffles per 16 bytes) so that steps and groups line up.
 //
-// A warp owns 8*R weight rows and a range of K.  Decode is bound by latency, so
+// A warp owns 8 weight rows and a range of K.  Decode is bound by latency, so
 // a warp keeps kAhead units of its range on their way (cp.async into a ring of
 // its own: a lane reads back only what it copied itself, so the loop has no
 // barrier, few registers and little code), and K is split until the ranges
@@ -103,7 +104,7 @@ __device__ __forceinline__ void line_up(uint4 &w, int t)
 }
 
 // Most units a block stages at once.
-template <int TOK> __host__ __device__ constexpr int max_chunk() { return TOK == 8 ? 48 : TOK == 16 ? 32 : 16; }
+template <int TOK> __host__ __device__ constexpr int max_chunk() { return TOK == 8 ? 48 : 32; }
 
 // 16 bytes of shared memory from the first n of src, the rest zero.
 __device__ __forceinline__ void copy_some(uint32_t dst, const void *src, int n)
@@ -135,26 +136,25 @@ struct Split {
     int split;    // blocks of a cluster
 };
 
-// TOK: tokens per pass (8, 16 or 32); R: slabs of 8 weight rows per warp.
-template <int TOK, int GM, int R>
-__global__ void __launch_bounds__(kRowWarps * kMaxKWarps * 32, TOK == 32 ? 2 : TOK == 16 ? 3 : 4)
+// TOK: tokens per pass, 8 or 16.  (Passes of 32 tokens, with 16 rows per warp,
+// took 24 us for 2560 -> 9728 at M = 32, two passes of 16 take 16 us.)
+template <int TOK, int GM>
+__global__ void __launch_bounds__(kRowWarps * kMaxKWarps * 32, TOK == 16 ? 3 : 4)
 gs_mma_kernel(const GsArgs a, const Split sp)
 {
-    constexpr int MT = TOK == 32 ? 2 : 1;        // 16-token tiles
-    constexpr int EL = TOK == 8 ? 2 : 4;         // C elements in use
-    constexpr int kElems = MT * R * EL;          // sums per lane
+    constexpr int EL = TOK == 8 ? 2 : 4;         // C elements in use: sums per lane
     constexpr int kRun = GM == kG256 ? 2 : 1;    // consecutive units that share a scale
     constexpr int kGroups = GM == kG32 ? 4 : GM == kG64 ? 2 : 1;  // groups of a unit
     constexpr int kSteps = 4 / kGroups;
-    constexpr int kPair = TOK == 32 ? kRun : 2;
-    constexpr int kRows = 8 * R * kRowWarps;     // weight rows of a block
+    constexpr int kPair = 2;                     // units multiplied together
+    constexpr int kRows = 8 * kRowWarps;         // weight rows of a block
     extern __shared__ __align__(16) uint8_t smem[];  // codes, scales, rings; then the sums that are added
     __shared__ float sx[TOK];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int rw = warp & (kRowWarps - 1), kw = warp / kRowWarps;
     const int g = lane >> 2, t = lane & 3;
     const int n_block = static_cast<int>(blockIdx.x) * kRows;
-    const int n0 = n_block + rw * (8 * R);
+    const int n0 = n_block + rw * 8;
     const int rank = blockIdx.y;
     const int u_lo = rank * sp.per * kRun;       // this block's units
     const int u_end = u_lo + sp.per * kRun;
@@ -162,9 +162,9 @@ gs_mma_kernel(const GsArgs a, const Split sp)
     const int stride = q_stride<GM>(sp.chunk);
     const int cgroups = sp.chunk * kGroups / kRun;  // groups staged at once
     const uint32_t q_base = tc::smem_u32(smem);
-    const uint32_t s_base = q_base + static_cast<uint32_t>(TOK * stride);  // [row warp, slab][group][8 rows]
-    const uint32_t s_mine = s_base + static_cast<uint32_t>(rw * R * cgroups * 32 + t * 8);
-    const uint32_t ring = s_base + static_cast<uint32_t>(kRows * cgroups * 4 + (warp * kAhead * R * 32 + lane) * 16);
+    const uint32_t s_base = q_base + static_cast<uint32_t>(TOK * stride);  // [row warp][group][8 rows]
+    const uint32_t s_mine = s_base + static_cast<uint32_t>(rw * cgroups * 32 + t * 8);
+    const uint32_t ring = s_base + static_cast<uint32_t>(kRows * cgroups * 4 + (warp * kAhead * 32 + lane) * 16);
 
     if (a.prefetch == 0) pdl_wait();
     pdl_trigger();
@@ -183,24 +183,15 @@ gs_mma_kernel(const GsArgs a, const Split sp)
         step = static_cast<int64_t>(gridDim.z) * TOK;
     }
     // this lane's row and piece of every unit, and the units that hold it
-    const uint8_t *piece[R];
-    int limit[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const int n = n0 + 8 * r + g;
-        piece[r] = packed + (n < a.N ? n : 0) * a.ldp + t * 16;
-        limit[r] = n < a.N ? (static_cast<int>((a.K + 31) >> 5) - t + 3) >> 2 : 0;
-    }
+    const bool row_on = n0 + g < a.N;
+    const uint8_t *piece = packed + (row_on ? n0 + g : 0) * a.ldp + t * 16;
+    const int limit = row_on ? (static_cast<int>((a.K + 31) >> 5) - t + 3) >> 2 : 0;
     bool waited = a.prefetch == 0;
 
     for (int64_t tok = lo; tok < hi; tok += step) {
-        float acc[MT][R][EL];
+        float acc[EL];
 #pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int i = 0; i < EL; ++i) acc[m][r][i] = 0.0f;
+        for (int e = 0; e < EL; ++e) acc[e] = 0.0f;
 
         for (int c0 = u_lo; c0 < u_hi; c0 += sp.chunk) {
             const int c1 = c0 + sp.chunk < u_hi ? c0 + sp.chunk : u_hi;
@@ -208,14 +199,10 @@ gs_mma_kernel(const GsArgs a, const Split sp)
             const int v0 = c0 + kw * share;
             const int v1 = v0 + share < c1 ? v0 + share : c1;
             // this lane's units to fetch: [v0, end); zeros from there on
-            int end[R];
-#pragma unroll
-            for (int r = 0; r < R; ++r) end[r] = limit[r] < v1 ? limit[r] : v1;
+            const int end = limit < v1 ? limit : v1;
             // unit u into its slot (addresses past `end` are not read)
             auto request = [&](int u) {
-                const uint32_t slot = ring + static_cast<uint32_t>((u & (kAhead - 1)) * (R * 512));
-#pragma unroll
-                for (int r = 0; r < R; ++r) copy_some(slot + r * 512, piece[r] + u * 64, u < end[r] ? 16 : 0);
+                copy_some(ring + static_cast<uint32_t>((u & (kAhead - 1)) * 512), piece + u * 64, u < end ? 16 : 0);
                 copy_commit();
             };
             auto request_first = [&] {
@@ -286,70 +273,55 @@ gs_mma_kernel(const GsArgs a, const Split sp)
 #pragma unroll 1
             for (int u0 = v0; u0 < v1; u0 += kPair) {
                 copy_wait<kAhead - kPair>();
-                uint4 x[kPair][R];
-                uint32_t q[kPair][MT][2][8];
+                uint4 x[kPair];
+                uint32_t q[kPair][2][8];
 #pragma unroll
                 for (int i = 0; i < kPair; ++i) {
-                    const uint32_t slot = ring + static_cast<uint32_t>(((u0 + i) & (kAhead - 1)) * (R * 512));
-#pragma unroll
-                    for (int r = 0; r < R; ++r) x[i][r] = tc::lds128(slot + r * 512);
+                    x[i] = tc::lds128(ring + static_cast<uint32_t>(((u0 + i) & (kAhead - 1)) * 512));
                     // (a last odd unit's partner has zero codes)
                     const uint32_t at = q_base + static_cast<uint32_t>((u0 + i - c0) * kUnit + g * stride);
-#pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        load_tokens<GM>(at + static_cast<uint32_t>(16 * m * stride), t, q[i][m][0]);
-                        if constexpr (TOK > 8) load_tokens<GM>(at + static_cast<uint32_t>((16 * m + 8) * stride), t, q[i][m][1]);
-                    }
+                    load_tokens<GM>(at, t, q[i][0]);
+                    if constexpr (TOK > 8) load_tokens<GM>(at + static_cast<uint32_t>(8 * stride), t, q[i][1]);
                 }
 #pragma unroll
                 for (int i = 0; i < kPair; ++i) {
-#pragma unroll
-                    for (int r = 0; r < R; ++r) line_up<GM>(x[i][r], t);
+                    line_up<GM>(x[i], t);
                     request(u0 + i + kAhead);  // the slot is in registers
                 }
 #pragma unroll
-                for (int r = 0; r < R; ++r)
+                for (int gr = 0; gr < kGroups; ++gr) {
+                    int32_t c[kPair / kRun][4];
 #pragma unroll
-                    for (int gr = 0; gr < kGroups; ++gr) {
-                        int32_t c[kPair / kRun][MT][4];
+                    for (int i = 0; i < kPair / kRun; ++i) c[i][0] = c[i][1] = c[i][2] = c[i][3] = 0;
 #pragma unroll
-                        for (int i = 0; i < kPair / kRun; ++i)
+                    for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-                            for (int m = 0; m < MT; ++m) c[i][m][0] = c[i][m][1] = c[i][m][2] = c[i][m][3] = 0;
-#pragma unroll
-                        for (int st = 0; st < kSteps; ++st)
-#pragma unroll
-                            for (int i = 0; i < kPair; ++i)
-#pragma unroll
-                                for (int m = 0; m < MT; ++m) {
-                                    const int k = gr * kSteps + st;
-                                    const uint32_t word = (&x[i][r].x)[k];
-                                    mma_s8(c[i / kRun][m], q[i][m][0][2 * k], TOK > 8 ? q[i][m][1][2 * k] : 0u,
-                                           q[i][m][0][2 * k + 1], TOK > 8 ? q[i][m][1][2 * k + 1] : 0u, i4_expand(word, 0),
-                                           i4_expand(word, 1));
-                                }
-#pragma unroll
-                        for (int i = 0; i < kPair / kRun; ++i) {
-                            if (u0 + i * kRun >= v1) break;
-                            // scales of the rows 2t and 2t + 1 that this lane's C columns belong to
-                            float s0, s1;
-                            const int gi = (u0 + i * kRun - c0) * kGroups / kRun + gr;
-                            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(s0), "=f"(s1)
-                                         : "r"(s_mine + static_cast<uint32_t>((r * cgroups + gi) * 32)));
-#pragma unroll
-                            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                                for (int e = 0; e < EL; ++e)
-                                    acc[m][r][e] = __fmaf_rn(e & 1 ? s1 : s0, __int2float_rn(c[i][m][e]), acc[m][r][e]);
+                        for (int i = 0; i < kPair; ++i) {
+                            const int k = gr * kSteps + st;
+                            const uint32_t word = (&x[i].x)[k];
+                            mma_s8(c[i / kRun], q[i][0][2 * k], TOK > 8 ? q[i][1][2 * k] : 0u, q[i][0][2 * k + 1],
+                                   TOK > 8 ? q[i][1][2 * k + 1] : 0u, i4_expand(word, 0), i4_expand(word, 1));
                         }
+#pragma unroll
+                    for (int i = 0; i < kPair / kRun; ++i) {
+                        if (u0 + i * kRun >= v1) break;
+                        // scales of the rows 2t and 2t + 1 that this lane's C columns belong to
+                        float s0, s1;
+                        const int gi = (u0 + i * kRun - c0) * kGroups / kRun + gr;
+                        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(s0), "=f"(s1)
+                                     : "r"(s_mine + static_cast<uint32_t>(gi * 32)));
+#pragma unroll
+                        for (int e = 0; e < EL; ++e)
+                            acc[e] = __fmaf_rn(e & 1 ? s1 : s0, __int2float_rn(c[i][e]), acc[e]);
                     }
+                }
             }
         }
 
-        // element e of lane (g, t): token 16 m + g + 8 (e >> 1), row 8 r + 2 t + (e & 1)
-        auto put = [&](int m, int r, int e, int ln, int row0, float v) {
-            const int tk = 16 * m + (ln >> 2) + 8 * (e >> 1);
-            const int n = row0 + 8 * r + 2 * (ln & 3) + (e & 1);
+        // element e of lane (g, t): token g + 8 (e >> 1), row 2 t + (e & 1)
+        auto put = [&](int e, int ln, int row0, float v) {
+            const int tk = (ln >> 2) + 8 * (e >> 1);
+            const int n = row0 + 2 * (ln & 3) + (e & 1);
             if (tok + tk < hi && n < a.N) {
                 const float f = __fmul_rn(v, sx[tk]);
                 if (a.y_bf16) static_cast<__nv_bfloat16 *>(a.y)[(tok + tk) * a.ldy + n] = __float2bfloat16_rn(f);
@@ -358,22 +330,13 @@ gs_mma_kernel(const GsArgs a, const Split sp)
         };
         if (sp.split == 1 && warps == kRowWarps) {
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int e = 0; e < EL; ++e) put(m, r, e, lane, n0, acc[m][r][e]);
+            for (int e = 0; e < EL; ++e) put(e, lane, n0, acc[e]);
         } else {
             __syncthreads();  // the staged codes are read
             float *sums = reinterpret_cast<float *>(smem);  // [K warp][element][row warp, lane]
-            constexpr int kTile = kElems * kRowWarps * 32;
+            constexpr int kTile = EL * kRowWarps * 32;
 #pragma unroll
-            for (int m = 0; m < MT; ++m)
-#pragma unroll
-                for (int r = 0; r < R; ++r)
-#pragma unroll
-                    for (int e = 0; e < EL; ++e)
-                        sums[kw * kTile + ((m * R + r) * EL + e) * (kRowWarps * 32) + rw * 32 + lane] = acc[m][r][e];
+            for (int e = 0; e < EL; ++e) sums[kw * kTile + e * (kRowWarps * 32) + rw * 32 + lane] = acc[e];
             if (sp.split > 1) tc::cluster_sync_all();
             else __syncthreads();
             // each block adds its share of the tile: K warps within ranks, ranks in order
@@ -395,8 +358,8 @@ gs_mma_kernel(const GsArgs a, const Split sp)
                 for (int p = 0; p < kMaxSplit; ++p)
 #pragma unroll
                     for (int k = 0; k < kMaxKWarps; ++k) v += part[p][k];
-                const int e = i / (kRowWarps * 32), th = i % (kRowWarps * 32);
-                put(e / (R * EL), e / EL % R, e % EL, th & 31, n_block + (th >> 5) * (8 * R), v);
+                const int th = i % (kRowWarps * 32);
+                put(i / (kRowWarps * 32), th & 31, n_block + (th >> 5) * 8, v);
             }
             if (sp.split > 1) tc::cluster_sync_all();  // peers have read this block's sums
         }
@@ -428,11 +391,11 @@ lowbit_status launch_clusters_y(void (*kernel)(KArgs...), dim3 grid, dim3 block,
     return launch_status();
 }
 
-template <int TOK, int GM, int R>
+template <int TOK, int GM>
 lowbit_status launch(const GsArgs &a, cudaStream_t st)
 {
-    constexpr int kRows = 8 * R * kRowWarps;
-    constexpr int kElems = (TOK == 32 ? 2 : 1) * R * (TOK == 8 ? 2 : 4);
+    constexpr int kRows = 8 * kRowWarps;
+    constexpr int kElems = TOK == 8 ? 2 : 4;
     constexpr int kRun = GM == kG256 ? 2 : 1;
     constexpr int kGroups = GM == kG32 ? 4 : GM == kG64 ? 2 : 1;
     const int64_t units = (a.K + kUnit - 1) / kUnit;
@@ -449,7 +412,7 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
     }
     // Ranges of K per row block: as many as make a warp's range about four
     // units, as long as all warps are resident at once.
-    const int64_t fit = static_cast<int64_t>(device_sm_count()) * (TOK == 8 ? 32 : TOK == 16 ? 24 : 16) / (slabs * active * kRowWarps);
+    const int64_t fit = static_cast<int64_t>(device_sm_count()) * (TOK == 8 ? 32 : 24) / (slabs * active * kRowWarps);
     int64_t ranges = (units + 3) / 4;
     if (ranges > fit) ranges = fit;
     if (ranges > runs) ranges = runs;
@@ -463,7 +426,7 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
     const int64_t chunk = per * kRun < max_chunk<TOK>() ? per * kRun : max_chunk<TOK>();
     const auto bytes = [](int64_t units_, int64_t kwarps_) {
         return static_cast<size_t>(TOK) * q_stride<GM>(static_cast<int>(units_)) +
-               static_cast<size_t>(kRows * units_ * kGroups / kRun * 4) + kRowWarps * kwarps_ * kAhead * R * 512;
+               static_cast<size_t>(kRows * units_ * kGroups / kRun * 4) + kRowWarps * kwarps_ * kAhead * 512;
     };
     size_t smem = bytes(chunk, kwarps);
     const size_t sums = static_cast<size_t>(kElems) * kRowWarps * kwarps * 32 * 4;
@@ -472,23 +435,26 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
     if (configured.get(dev, [&] {
-            return cudaFuncSetAttribute(gs_mma_kernel<TOK, GM, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(gs_mma_kernel<TOK, GM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(bytes(max_chunk<TOK>(), kMaxKWarps))) == cudaSuccess ? 1 : 0;
         }) <= 0)
         return LOWBIT_ERR_CUDA;
     const Split sp = {static_cast<int>(units), static_cast<int>(per), static_cast<int>(chunk), static_cast<int>(split)};
-    return launch_clusters_y(gs_mma_kernel<TOK, GM, R>,
+    return launch_clusters_y(gs_mma_kernel<TOK, GM>,
                              dim3(static_cast<unsigned>(slabs), static_cast<unsigned>(split), static_cast<unsigned>(ztiles)),
                              dim3(static_cast<unsigned>(kRowWarps * kwarps * 32)), smem, st, static_cast<unsigned>(split), a,
                              sp);
 }
 
-template <int TOK, int R>
+template <int TOK>
 lowbit_status launch_g(const GsArgs &a, cudaStream_t st)
 {
-    if (a.gshift == 8) return launch<TOK, kG256, R>(a, st);
-    if (a.gshift == 7) return launch<TOK, kG128, R>(a, st);
-    return a.gshift == 6 ? launch<TOK, kG64, R>(a, st) : launch<TOK, kG32, R>(a, st);
+    switch (a.gshift) {
+    case 5: return launch<TOK, kG32>(a, st);
+    case 6: return launch<TOK, kG64>(a, st);
+    case 7: return launch<TOK, kG128>(a, st);
+    default: return launch<TOK, kG256>(a, st);
+    }
 }
 
 }  // namespace gsm
@@ -496,9 +462,7 @@ lowbit_status launch_g(const GsArgs &a, cudaStream_t st)
 lowbit_status gs_mma_launch(const GsArgs &a, cudaStream_t st)
 {
     const int64_t per = a.offsets != nullptr ? (a.M + a.E - 1) / a.E : a.M;
-    if (per <= 8) return gsm::launch_g<8, 1>(a, st);
-    if (per <= 16) return gsm::launch_g<16, 1>(a, st);
-    return gsm::launch_g<32, 2>(a, st);
+    return per <= 8 ? gsm::launch_g<8>(a, st) : gsm::launch_g<16>(a, st);
 }
 
 }  // namespace lowbit
