@@ -56,12 +56,12 @@ lowbit_status check_slots(const void *pos, int64_t T, int k, int64_t rows)
     return aligned(pos, 4) ? LOWBIT_OK : LOWBIT_ERR_ALIGNMENT;
 }
 
-// The kernel for a call, by its estimated time in ns.  Measured on B200 (256 to
-// 9728 features, 16 to 512 tokens): the warp-level kernel takes about 4.5 us
-// and 0.19 us per million weights and pass of 16 tokens; the tcgen05 one 4.6 us
-// and 0.5 us per 128 codes of K and round of its 256 x 256 tiles over the SM
-// pairs.  (At 64 tokens 1280 -> 3584 takes 8.7 us on the first and 9.6 on the
-// second, 2560 -> 9728 25 and 15 us, 9728 -> 2560 30 and 43 us.)  Experts are
+// The kernel for a call, by its estimated time in ns, measured on a B200 (512 to
+// 9728 features, 1 to 4096 tokens).  The warp-level kernel takes about 4.5 us,
+// 0.5 us per 1000 codes of K and, per million weights and pass of 16 tokens,
+// 0.21 us (groups of 128 and 256) or 0.33 us; gs_gemm_plan has the tcgen05
+// kernel's.  (Groups of 128, 64 tokens: 1280 -> 3584 takes 8.6 us on either,
+// 2560 -> 9728 27.5 and 14.9 us, 4096 -> 512 7.3 and 10.9 us.)  Experts are
 // taken to share the rows evenly; any distribution is correct on both.
 lowbit_status gs_product(const GsArgs &a, cudaStream_t st)
 {
@@ -69,11 +69,10 @@ lowbit_status gs_product(const GsArgs &a, cudaStream_t st)
     const int64_t active = a.offsets == nullptr ? 1 : a.E < a.M ? a.E : a.M;
     const int64_t rows = (a.M + active - 1) / active;
     if (rows <= 16) return gs_mma_launch(a, st);
-    const double mma = 4500.0 + 190.0 * 1e-6 * static_cast<double>(a.N) * static_cast<double>(a.K) *
-                                    static_cast<double>(active * ((rows + 15) / 16));
-    const int64_t tiles = active * ((rows + 255) / 256) * ((a.N + 255) / 256), pairs = device_sm_count() / 2;
-    const double gemm = 4600.0 + 500.0 * static_cast<double>((a.K + 127) / 128 * ((tiles + pairs - 1) / pairs));
-    return mma <= gemm ? gs_mma_launch(a, st) : gs_gemm_launch(a, st);
+    const double pass = (a.gshift >= 7 ? 210.0 : 330.0) * 1e-6 * static_cast<double>(a.N) * static_cast<double>(a.K);
+    const double mma = 4500.0 + 0.5 * static_cast<double>(a.K) + pass * static_cast<double>(active * ((rows + 15) / 16));
+    const GsGemmPlan p = gs_gemm_plan(a);
+    return mma <= p.ns ? gs_mma_launch(a, st) : gs_gemm_launch(a, p, st);
 }
 
 }  // namespace

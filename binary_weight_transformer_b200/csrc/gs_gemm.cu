@@ -17,7 +17,9 @@
 // A cluster of two CTAs computes a tile of 256 weight rows x NT tokens.  CTA r
 // stages its 128 rows' packed codes and its half of the tokens with TMA,
 // expands the codes (c << 4) into its own shared memory (the rows of A it
-// owns) and drains its own 128 lanes.  The even CTA issues the MMAs.
+// owns) and drains its own 128 lanes.  The even CTA issues the MMAs.  Where
+// there are few tiles, a cluster has two or four such pairs, each with a part
+// of K, whose fp32 sums are added through distributed shared memory.
 //
 // Warps (512 threads): 0 TMA, 1 MMA issue and tensor memory, 2-3 idle;
 // 4-7 expanders; 8-15 drain, two per 32-lane quarter, half the columns each.
@@ -81,12 +83,13 @@ struct Tile {
 template <int NT>
 struct Tiles {
     const Plan *plan;
-    uint32_t id, total, num_w;
+    uint32_t id, step, total, num_w;
     int e = 0, dense_rows;
 
-    __device__ __forceinline__ Tiles(const Plan *p, const GsArgs &a) : plan(p)
+    __device__ __forceinline__ Tiles(const Plan *p, const GsArgs &a, uint32_t split) : plan(p)
     {
-        id = blockIdx.x >> 1;
+        id = blockIdx.x / (2 * split);
+        step = gridDim.x / (2 * split);
         num_w = static_cast<uint32_t>((a.N + 2 * kRows - 1) / (2 * kRows));
         total = static_cast<uint32_t>(p->start[a.E]) * num_w;
         dense_rows = a.offsets == nullptr ? static_cast<int>(a.M) : 0;
@@ -99,7 +102,7 @@ struct Tiles {
             t.row0 = static_cast<int>(id / num_w) * NT;
             t.hi = dense_rows;
             t.w0 = static_cast<int>(id % num_w) * (2 * kRows);
-            id += gridDim.x >> 1;
+            id += step;
             return true;
         }
         const int tt = static_cast<int>(id / num_w);
@@ -108,7 +111,7 @@ struct Tiles {
         t.row0 = plan->lo[e] + (tt - plan->start[e]) * NT;
         t.hi = plan->hi[e];
         t.w0 = static_cast<int>(id % num_w) * (2 * kRows);
-        id += gridDim.x >> 1;
+        id += step;
         return true;
     }
 };
@@ -132,12 +135,13 @@ __device__ __forceinline__ void mma_i8_pair(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
-// Arrive on both CTAs' barrier when the MMAs issued so far are complete.
-__device__ __forceinline__ void commit_both(uint64_t *bar)
+// Arrive on the barrier of both CTAs of the pair (mask) when the MMAs issued so
+// far are complete.
+__device__ __forceinline__ void commit_both(uint64_t *bar, uint16_t mask)
 {
     asm volatile(
         "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
-        ::"r"(smem_u32(bar)), "h"(static_cast<uint16_t>(0x3)) : "memory");
+        ::"r"(smem_u32(bar)), "h"(mask) : "memory");
 }
 
 __device__ __forceinline__ void commit_self(uint64_t *bar)
@@ -324,19 +328,95 @@ __device__ __forceinline__ void store_staged(float *p, int64_t ldy, int left, ui
     }
 }
 
+// Where a drain warp's columns go: weight rows n0 + lane, `left` tokens from row0.
+struct Target {
+    void *y;
+    int bf16;
+    int64_t ldy, row0;
+    int n0;
+    int64_t N;
+    int left;
+    bool vec;
+    uint32_t sx, stage;
+    int lane;
+};
+
 template <typename T, int NC>
-__device__ __forceinline__ void store_columns(void *y, int64_t ldy, int64_t row0, int n0, int64_t N, int left, bool vec,
-                                              uint32_t sx, uint32_t stage, int lane, const float2 (&acc)[NC / 2])
+__device__ __forceinline__ void store_as_type(const Target &t, const float2 (&acc)[NC / 2])
 {
-    T *p = static_cast<T *>(y) + row0 * ldy + n0;
-    if (vec && n0 + 32 <= N) store_staged<NC>(p, ldy, left, sx, stage, lane, acc);
-    else if (n0 + lane < N) store_elements<T, NC>(p + lane, ldy, left, sx, acc);
+    T *p = static_cast<T *>(t.y) + t.row0 * t.ldy + t.n0;
+    if (t.vec && t.n0 + 32 <= t.N) store_staged<NC>(p, t.ldy, t.left, t.sx, t.stage, t.lane, acc);
+    else if (t.n0 + t.lane < t.N) store_elements<T, NC>(p + t.lane, t.ldy, t.left, t.sx, acc);
+}
+
+template <int NC>
+__device__ __forceinline__ void store_columns(const Target &t, const float2 (&acc)[NC / 2])
+{
+    if (t.bf16) store_as_type<__nv_bfloat16, NC>(t, acc);
+    else store_as_type<float, NC>(t, acc);
+}
+
+// K split over the S pairs of a cluster: pair p keeps the columns [p, p + 1) *
+// NC / S of each drain warp's NC, adds the other pairs' sums of them, pairs in
+// order, and stores them.  The others' sums arrive in the ring of the CTA
+// (idle by then) at [slot][warp][column / 4][lane] 16 bytes.  Every warp of the
+// cluster takes part in the two barriers.
+template <int NC, int S>
+__device__ __forceinline__ void add_and_store(const Target &t, const float2 (&acc)[NC / 2], int sk, uint32_t rank, int w,
+                                              uint32_t ring, bool ok)
+{
+    constexpr int C = NC / S;
+    const uint32_t mine = ring + static_cast<uint32_t>((w * (C / 4) * 32 + t.lane) * 16);
+    constexpr uint32_t kSlot = kDrainWarps * (C / 4) * 32 * 16;
+    static_assert((S - 1) * kSlot <= stages<2 * NC>() * q_bytes<2 * NC>(), "the sums must fit the ring");
+    cluster_sync_all();  // every CTA's rings are idle
+    float2 out[C / 2];
+#pragma unroll
+    for (int p = 0; p < S; ++p) {
+        if (p == sk) {
+#pragma unroll
+            for (int j = 0; j < C / 2; ++j) out[j] = acc[p * (C / 2) + j];
+        } else {
+            const uint32_t to = map_to_peer(mine, 2 * static_cast<uint32_t>(p) + rank) + (sk < p ? sk : sk - 1) * kSlot;
+#pragma unroll
+            for (int j = 0; j < C / 4; ++j) {
+                const float2 a = acc[p * (C / 2) + 2 * j], b = acc[p * (C / 2) + 2 * j + 1];
+                st_cluster128(to + j * 512, __float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x),
+                              __float_as_uint(b.y));
+            }
+        }
+    }
+    cluster_sync_all();  // the sums have arrived
+    if (!ok) return;
+#pragma unroll
+    for (int j = 0; j < C / 4; ++j) {
+        uint4 part[S - 1];
+#pragma unroll
+        for (int p = 0; p < S - 1; ++p) part[p] = lds128(mine + p * kSlot + j * 512);
+        float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        const float own[4] = {out[2 * j].x, out[2 * j].y, out[2 * j + 1].x, out[2 * j + 1].y};
+#pragma unroll
+        for (int p = 0; p < S; ++p)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float before = p > 0 ? __uint_as_float((&part[p - 1].x)[i]) : 0.0f;  // slot of pair p where p > sk
+                const float after = p < S - 1 ? __uint_as_float((&part[p < S - 1 ? p : 0].x)[i]) : 0.0f;
+                v[i] += p == sk ? own[i] : p > sk ? before : after;
+            }
+        out[2 * j] = make_float2(v[0], v[1]);
+        out[2 * j + 1] = make_float2(v[2], v[3]);
+    }
+    const Target part = {t.y,   t.bf16, t.ldy,  t.row0 + sk * C, t.n0, t.N, t.left - sk * C, t.vec, t.sx + sk * C * 4,
+                         t.stage, t.lane};
+    store_columns<C>(part, out);
+    __syncwarp();
 }
 
 // NT tokens per tile; PER MMAs of 32 codes per group (group / 32); SB: bf16 scales.
 template <int NT, int PER, bool SB>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_p, const GsArgs a)
+__global__ void __launch_bounds__(kThreads, 1)
+gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_p, const GsArgs a,
+               const int split, const int per_kb)
 {
     constexpr int ST = stages<NT>(), SE = kExpStages;
     constexpr int Q_BYTES = q_bytes<NT>();
@@ -364,8 +444,11 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     Plan *plan = reinterpret_cast<Plan *>(acc_full + 12);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t rank = cluster_rank();
+    // CTA `rank` of pair `sk` of the `split` pairs of a cluster
+    const uint32_t crank = cluster_rank(), rank = crank & 1u, lead = crank & ~1u;
+    const int sk = static_cast<int>(crank >> 1);
     const bool leader = rank == 0;
+    const uint16_t pair_mask = static_cast<uint16_t>(0x3u << lead);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -421,20 +504,22 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     }
     __syncthreads();
 
+    // this pair's K blocks
     const int nkb = static_cast<int>((a.K + BK - 1) / BK);
+    const int kb0 = sk * per_kb, kb1 = kb0 + per_kb < nkb ? kb0 + per_kb : nkb;
     if (warp < 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLeanRegs));
         if (warp == 0) {
             // ---------------- TMA producer (both CTAs) ----------------
             if (lane == 0) {
-                Tiles<NT> tiles(plan, a);
+                Tiles<NT> tiles(plan, a, split);
                 Tile tl;
                 uint32_t g = 0;
                 bool ok = true;
                 while (ok && tiles.next(tl)) {
                     const int t0 = tl.row0 + static_cast<int>(rank) * SUB;
                     const int w0 = tl.w0 + static_cast<int>(rank) * kRows;
-                    for (int kb = 0; kb < nkb; ++kb, ++g) {
+                    for (int kb = kb0; kb < kb1; ++kb, ++g) {
                         const int s = g % ST;
                         if (!wait_bar(&mma_done[s], ((g / ST) & 1u) ^ 1u, abort_flag, a.status)) { ok = false; break; }
                         mbar_arrive_expect_tx(&full_tma[s], Q_BYTES + P_BYTES);
@@ -454,7 +539,7 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             if (leader && lane == 0) {
                 const uint64_t qdesc0 = sw128_desc(smem_u32(sQ));
                 const uint64_t edesc0 = sw128_desc(smem_u32(sE));
-                Tiles<NT> tiles(plan, a);
+                Tiles<NT> tiles(plan, a, split);
                 Tile tl;
                 uint32_t g = 0, h = 0;  // K blocks and groups so far
                 bool ok = true;
@@ -463,12 +548,12 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 // long to issue.  K blocks are whole: past K the token codes
                 // are zero.
                 while (ok && tiles.next(tl)) {
-                    for (int kb = 0; ok && kb < nkb; ++kb, ++g) {
+                    for (int kb = kb0; ok && kb < kb1; ++kb, ++g) {
                         const int s1 = g % ST, s2 = g % SE;
                         const uint64_t qdesc = qdesc0 + static_cast<uint64_t>((s1 * Q_BYTES) >> 4);
                         const uint64_t edesc = edesc0 + static_cast<uint64_t>((s2 * E_BYTES) >> 4);
-                        const bool opens = PER <= 4 || (kb & 1) == 0;
-                        const bool closes = PER <= 4 || (kb & 1) != 0 || kb + 1 == nkb;
+                        const bool opens = PER <= 4 || ((kb - kb0) & 1) == 0;
+                        const bool closes = PER <= 4 || ((kb - kb0) & 1) != 0 || kb + 1 == kb1;
 #pragma unroll
                         for (int f = 0; f < FPB; ++f) {
                             const int b = h % NB;
@@ -486,11 +571,11 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                                             qdesc + static_cast<uint64_t>(kk * (UMMA_K >> 4)), idesc<NT>(),
                                             kk == f * 4 / FPB && opens ? 0u : 1u);
                             if (closes) {
-                                commit_both(&acc_full[b]);
+                                commit_both(&acc_full[b], pair_mask);
                                 ++h;
                             }
                         }
-                        if (ok) commit_both(&mma_done[s1]);
+                        if (ok) commit_both(&mma_done[s1], pair_mask);
                     }
                 }
                 commit_self(drain);
@@ -500,13 +585,13 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             // ---------------- expanders: own 128 weight rows ----------------
             const int et = threadIdx.x - 128;
             const uint32_t p_base = smem_u32(sP), e_base = smem_u32(sE);
-            const uint32_t full_exp_leader = map_to_peer(smem_u32(full_exp), 0);
-            Tiles<NT> tiles(plan, a);
+            const uint32_t full_exp_leader = map_to_peer(smem_u32(full_exp), lead);
+            Tiles<NT> tiles(plan, a, split);
             Tile tl;
             uint32_t g = 0;
             bool ok = true;
             while (ok && tiles.next(tl)) {
-                for (int kb = 0; kb < nkb; ++kb, ++g) {
+                for (int kb = kb0; kb < kb1; ++kb, ++g) {
                     const int s1 = g % ST, s2 = g % SE;
                     if (!wait_bar(&full_tma[s1], (g / ST) & 1u, abort_flag, a.status)) { ok = false; break; }
                     if (g >= static_cast<uint32_t>(SE)) {
@@ -525,12 +610,13 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kDrainRegs));
         const int quarter = warp & 3, x = (warp - 8) >> 2;
         float *sx = sX + (warp - 8) * SUB;
-        const uint32_t empty_leader = map_to_peer(smem_u32(acc_empty), 0);
+        const uint32_t empty_leader = map_to_peer(smem_u32(acc_empty), lead);
         const uint32_t tacc = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(x * SUB);
         const int groups = static_cast<int>((a.K - 1) >> a.gshift) + 1;
-        const int ends = PER == 8 ? (nkb + 1) / 2 : nkb * FPB;  // groups of the whole K blocks
+        const int g_first = PER == 8 ? kb0 / 2 : kb0 * FPB;
+        const int ends = PER == 8 ? (kb1 - kb0 + 1) / 2 : (kb1 - kb0) * FPB;  // groups of this pair's K blocks
         const bool vec = reinterpret_cast<uintptr_t>(a.y) % 16 == 0 && a.ldy % (a.y_bf16 ? 8 : 4) == 0;
-        Tiles<NT> tiles(plan, a);
+        Tiles<NT> tiles(plan, a, split);
         Tile tl;
         uint32_t h = 0;  // groups so far
         bool ok = true;
@@ -540,7 +626,7 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
             const ScaleRow<SB> scales(a.s_g, tl.e * a.sstride + static_cast<int64_t>(row_on ? n : 0) * a.lds);
             const int row0 = tl.row0 + x * SUB;  // this warp's first token
             const int left = tl.hi - row0;
-            float s_next = scales.at(0);
+            float s_next = scales.at(g_first);
             float xr[SUB / 32];  // token scales, needed (in shared memory) when the tile is stored
 #pragma unroll
             for (int i = 0; i < SUB / 32; ++i) xr[i] = lane + 32 * i < left ? ld_act_f32(a.s_x + row0 + lane + 32 * i) : 0.0f;
@@ -563,15 +649,15 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 return __shfl_sync(0xffffffffu, ready, 0) != 0;
             };
             ok = wait_full(h);
-            if (!ok) break;
             tc_fence_after();
             tmem_ld16(tacc + (h % NB) * NT, v[0]);
             tmem_wait16(v[0]);
-            for (int gr = 0; gr < ends; ++gr, ++h) {
+            for (int gr = 0; ok && gr < ends; ++gr, ++h) {
                 const uint32_t b = h % NB, bn = (h + 1) % NB;
                 const bool more = gr + 1 < ends;
-                const float s = s_next;
-                s_next = scales.at(gr + 1 < groups ? gr + 1 : 0);
+                const float s = g_first + gr < groups ? s_next : 0.0f;
+                // groups past the row's last, of the last K block, add zeros
+                s_next = scales.at(g_first + gr + 1 < groups ? g_first + gr + 1 : 0);
                 bool polled = true;
 #pragma unroll
                 for (int c = 0; c < NCH; ++c) {
@@ -587,7 +673,6 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         next = tacc + (more ? bn : b) * NT;
                     }
                     tmem_ld16(next, v[(c + 1) & 1]);
-                    // groups past the row's last hold zero sums
 #pragma unroll
                     for (int j = 0; j < CH / 2; ++j) fma2(acc[CH / 2 * c + j], s, v[c & 1][2 * j], v[c & 1][2 * j + 1]);
                     tmem_wait16(v[(c + 1) & 1]);
@@ -598,22 +683,29 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                         if (lane == 0) mbar_arrive_remote(empty_leader + b * 8);
                     }
                 }
-                if (!ok) break;
             }
-            if (!ok) break;
-            {
-                // the factor 16 of the shifted codes leaves with the token scale
+            // the factor 16 of the shifted codes leaves with the token scale
 #pragma unroll
-                for (int i = 0; i < SUB / 32; ++i) sx[lane + 32 * i] = __fmul_rn(xr[i], 0.0625f);
-                __syncwarp();
-                const uint32_t stage = smem_u32(sStage) + static_cast<uint32_t>((warp - 8) * kStageBytes);
-                if (a.y_bf16)
-                    store_columns<__nv_bfloat16, SUB>(a.y, a.ldy, row0, n - lane, a.N, left, vec, smem_u32(sx), stage, lane, acc);
-                else
-                    store_columns<float, SUB>(a.y, a.ldy, row0, n - lane, a.N, left, vec, smem_u32(sx), stage, lane, acc);
-            }
+            for (int i = 0; i < SUB / 32; ++i) sx[lane + 32 * i] = __fmul_rn(xr[i], 0.0625f);
             __syncwarp();
+            const uint32_t stage = smem_u32(sStage) + static_cast<uint32_t>((warp - 8) * kStageBytes);
+            const Target to = {a.y, a.y_bf16, a.ldy, row0, n - lane, a.N, left, vec, smem_u32(sx), stage, lane};
+            if (split == 1) {
+                if (!ok) break;
+                store_columns<SUB>(to, acc);
+                __syncwarp();
+            } else {
+                // one tile per cluster: its rings are idle now
+                if (split == 2) add_and_store<SUB, 2>(to, acc, sk, rank, warp - 8, smem_u32(sQ), ok);
+                else add_and_store<SUB, 4>(to, acc, sk, rank, warp - 8, smem_u32(sQ), ok);
+                break;
+            }
         }
+    }
+    if (split > 1 && warp < 8) {
+        __syncwarp();
+        cluster_sync_all();  // the two of add_and_store
+        cluster_sync_all();
     }
 
     __syncwarp();
@@ -627,25 +719,32 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
     }
 }
 
-// Pairs that can be resident at once, found (with the shared-memory attribute
-// set) on the first launch on each device.
+// Clusters of `split` pairs that can be resident at once, found (with the
+// shared-memory attribute set) on the first launch on each device.
 template <int NT, int PER, bool SB>
-int resident_pairs(int dev)
+int resident_clusters(int dev, int split)
 {
     constexpr size_t smem = smem_bytes<NT>();
     static_assert(smem <= 232448, "shared memory budget");
-    static PerDevice pairs;
-    return pairs.get(dev, [&] {
+    static PerDevice clusters[3];
+    return clusters[split >> 1].get(dev, [&] {
         if (cudaFuncSetAttribute(gs_gemm_kernel<NT, PER, SB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  static_cast<int>(smem)) != cudaSuccess)
             return 0;
         // the register split needs all of the launch's registers
         cudaFuncAttributes at;
         if (cudaFuncGetAttributes(&at, gs_gemm_kernel<NT, PER, SB>) != cudaSuccess || at.numRegs < kLaunchRegs) return 0;
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = static_cast<unsigned>(2 * split);
+        attr.val.clusterDim.y = 1;
+        attr.val.clusterDim.z = 1;
         cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(2 * static_cast<unsigned>(device_sm_count() / 2));
+        cfg.gridDim = dim3(static_cast<unsigned>(2 * split) * static_cast<unsigned>(device_sm_count() / (2 * split)));
         cfg.blockDim = dim3(kThreads);
         cfg.dynamicSmemBytes = smem;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
         int n = 0;
         return cudaOccupancyMaxActiveClusters(&n, gs_gemm_kernel<NT, PER, SB>, &cfg) == cudaSuccess ? n : 0;
     });
@@ -668,39 +767,40 @@ bool make_weight_map(CUtensorMap *map, const GsArgs &a)
 }
 
 template <int NT, int PER, bool SB>
-lowbit_status launch(const GsArgs &a, cudaStream_t st)
+lowbit_status launch(const GsArgs &a, const GsGemmPlan &p, cudaStream_t st)
 {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
-    const int64_t resident = resident_pairs<NT, PER, SB>(dev);
+    const int64_t resident = resident_clusters<NT, PER, SB>(dev, p.split);
     if (resident <= 0) return LOWBIT_ERR_CUDA;
     CUtensorMap mq, mp;
     if (!make_map_2d(&mq, a.q, static_cast<uint64_t>(a.K), static_cast<uint64_t>(a.M), static_cast<uint64_t>(a.ldq), BK,
                      NT / 2, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_weight_map(&mp, a))
         return LOWBIT_ERR_CUDA;
-    // experts: their row counts are on the device; at most this many token tiles
-    const int64_t token_tiles = a.M / NT + (a.offsets != nullptr ? a.E : 1);
-    int64_t pairs = token_tiles * ((a.N + 2 * kRows - 1) / (2 * kRows));
-    if (pairs > resident) pairs = resident;
-    return launch_pdl(gs_gemm_kernel<NT, PER, SB>, dim3(static_cast<unsigned>(2 * pairs)), dim3(kThreads), smem_bytes<NT>(), st,
-                      0, mq, mp, a);
+    // Experts: their row counts are on the device; at most this many tiles.
+    const int64_t token_tiles = a.offsets != nullptr ? a.M / NT + a.E : (a.M + NT - 1) / NT;
+    const int64_t tiles = token_tiles * ((a.N + 2 * kRows - 1) / (2 * kRows));
+    // a cluster of several pairs does one tile
+    const int64_t clusters = p.split > 1 || tiles < resident ? tiles : resident;
+    return launch_pdl(gs_gemm_kernel<NT, PER, SB>, dim3(static_cast<unsigned>(2 * p.split * clusters)), dim3(kThreads),
+                      smem_bytes<NT>(), st, static_cast<unsigned>(2 * p.split), mq, mp, a, p.split, p.per_kb);
 }
 
 template <int NT, int PER>
-lowbit_status launch_s(const GsArgs &a, cudaStream_t st)
+lowbit_status launch_s(const GsArgs &a, const GsGemmPlan &p, cudaStream_t st)
 {
-    return a.s_bf16 ? launch<NT, PER, true>(a, st) : launch<NT, PER, false>(a, st);
+    return a.s_bf16 ? launch<NT, PER, true>(a, p, st) : launch<NT, PER, false>(a, p, st);
 }
 
 template <int NT>
-lowbit_status launch_g(const GsArgs &a, cudaStream_t st)
+lowbit_status launch_g(const GsArgs &a, const GsGemmPlan &p, cudaStream_t st)
 {
     switch (a.gshift) {
-    case 5: return launch_s<NT, 1>(a, st);
-    case 6: return launch_s<NT, 2>(a, st);
-    case 7: return launch_s<NT, 4>(a, st);
-    default: return launch_s<NT, 8>(a, st);
+    case 5: return launch_s<NT, 1>(a, p, st);
+    case 6: return launch_s<NT, 2>(a, p, st);
+    case 7: return launch_s<NT, 4>(a, p, st);
+    default: return launch_s<NT, 8>(a, p, st);
     }
 }
 
@@ -708,10 +808,56 @@ lowbit_status launch_g(const GsArgs &a, cudaStream_t st)
 
 lowbit_status set_wait_limit_gs(long long cycles) { return tc::set_wait_limit_here(cycles); }
 
-lowbit_status gs_gemm_launch(const GsArgs &a, cudaStream_t st)
+// Clusters of `split` pairs that run at once on the current device.  (All
+// variants of the kernel take a whole SM per CTA.)
+static int gs_gemm_clusters(int split)
 {
-    const int64_t rows = a.offsets != nullptr ? a.M / a.E : a.M;
-    return rows > 128 ? gsg::launch_g<256>(a, st) : gsg::launch_g<128>(a, st);
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess ? gsg::resident_clusters<256, 4, false>(dev, split) : 0;
+}
+
+// Tile width and split of K with the least estimated time:
+//   4200 + waves * (blocks * block + store) + merge    [ns]
+// for `waves` tiles per cluster of `blocks` K blocks of 128 each, measured on a
+// B200.  A block takes 470 ns for its copies, expansion and MMAs, or, where
+// more groups end in it, as long as their drain: 150 + 260 per group (NT =
+// 128), 100 + 480 (256).  Storing a tile takes 700 or 1900, adding 2 pairs' sums
+// 1100 or 1700, 4 pairs' 2600 or 4500.  K is split only where every tile has a
+// cluster at once, with four K blocks or more per pair.  9728 -> 2560 codes,
+// groups of 128: 128 tokens take 42 us on 10 tiles of 128 and 17.3 with K split
+// over four pairs; 256 tokens 42 on 20 tiles, 22.3 on 10 tiles of 256 x 4 pairs.
+GsGemmPlan gs_gemm_plan(const GsArgs &a)
+{
+    using namespace gsg;
+    const int64_t nkb = (a.K + BK - 1) / BK, wt = (a.N + 2 * kRows - 1) / (2 * kRows);
+    const int64_t pairs = device_sm_count() / 2;
+    const int64_t unit = a.gshift == 8 ? 2 : 1;  // a group's K blocks stay together
+    const double ends = 128.0 / static_cast<double>(1 << a.gshift);
+    GsGemmPlan best = {0, 1, 0, 0.0};
+    for (int nt = 128; nt <= 256; nt *= 2) {
+        const bool wide = nt == 256;
+        const double drain = wide ? 100.0 + 480.0 * ends : 150.0 + 260.0 * ends, block = drain > 470.0 ? drain : 470.0;
+        // experts: an expert's last tile is half full on average
+        const int64_t active = a.E < a.M ? a.E : a.M, rows = a.M / active;
+        const int64_t tiles = wt * (a.offsets == nullptr ? (a.M + nt - 1) / nt : active * (1 + (rows - nt / 2 > 0 ? rows - nt / 2 : 0) / nt));
+        for (int split = 1; split <= 4; split *= 2) {
+            const int64_t per = ((nkb + split - 1) / split + unit - 1) / unit * unit;
+            if (split > 1 && (a.offsets != nullptr || per < 4 || (split - 1) * per >= nkb ||
+                              tiles > gs_gemm_clusters(split)))
+                break;
+            const int64_t waves = split > 1 ? 1 : (tiles + pairs - 1) / pairs;
+            const double merge = split == 1 ? 0.0 : split == 2 ? (wide ? 1700.0 : 1100.0) : (wide ? 4500.0 : 2600.0);
+            const double ns = 4200.0 + merge + static_cast<double>(waves) *
+                                                   (static_cast<double>(per) * block + (wide ? 1900.0 : 700.0));
+            if (best.nt == 0 || ns < best.ns) best = {nt, split, static_cast<int>(per), ns};
+        }
+    }
+    return best;
+}
+
+lowbit_status gs_gemm_launch(const GsArgs &a, const GsGemmPlan &p, cudaStream_t st)
+{
+    return p.nt == 256 ? gsg::launch_g<256>(a, p, st) : gsg::launch_g<128>(a, p, st);
 }
 
 }  // namespace lowbit

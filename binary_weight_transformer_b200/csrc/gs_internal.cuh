@@ -79,7 +79,14 @@ __device__ __forceinline__ void divide(int64_t id, int64_t d, int64_t &quotient,
 bool gs_gemv_takes(const GsArgs &a);
 lowbit_status gs_gemv_launch(const GsArgs &a, cudaStream_t st);
 lowbit_status gs_mma_launch(const GsArgs &a, cudaStream_t st);
-lowbit_status gs_gemm_launch(const GsArgs &a, cudaStream_t st);
+// How the tcgen05 kernel would run a call: tokens per tile, pairs that share a
+// tile's K, K blocks of 128 for each, and the time that it is expected to take.
+struct GsGemmPlan {
+    int nt, split, per_kb;
+    double ns;
+};
+GsGemmPlan gs_gemm_plan(const GsArgs &a);
+lowbit_status gs_gemm_launch(const GsArgs &a, const GsGemmPlan &p, cudaStream_t st);
 lowbit_status gs_pack_launch(const void *w, int w_bf16, int64_t N, int64_t K, int64_t ldw, int gshift, uint8_t *packed,
                              int64_t ldp, void *s_g, int s_bf16, int64_t lds, int32_t *status, cudaStream_t st);
 lowbit_status gs_unpack_launch(const uint8_t *packed, int64_t ldp, const void *s_g, int s_bf16, int64_t lds, int64_t N,

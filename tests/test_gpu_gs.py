@@ -166,6 +166,14 @@ def test_linear_many_tokens(M, K, N, group):
     check_linear(M, K, N, group, bwt.BF16, bwt.BF16)
 
 
+@pytest.mark.parametrize("M,K,N", [(100, 5000, 200), (129, 4096, 96), (300, 2560, 257), (40, 9728, 513), (200, 16385, 31)])
+@pytest.mark.parametrize("group", bwt.GS_GROUPS)
+def test_linear_deep(M, K, N, group):
+    """Few tiles over a long K: each tile's K is split over several SM pairs."""
+    check_linear(M, K, N, group, bwt.F32, bwt.F32)
+    check_linear(M, K, N, group, bwt.BF16, bwt.BF16, ldy=N + 7)
+
+
 @pytest.mark.parametrize("M", [1, 12, 200])
 def test_linear_strides(M):
     check_linear(M, 500, 50, 64, bwt.BF16, bwt.BF16, stable=True, lds=11, ldy=57, ldp=320)
@@ -189,6 +197,22 @@ def test_linear_extreme_codes_and_scales(M):
     want, mag = ref.linear(q, s_x, codes, scales, group)
     assert (np.abs(got.double().cpu().numpy() - want) <= ref.linear_bound(want, mag, K // group, False)).all()
     assert (got[:, 3] == 0).all()
+
+
+@pytest.mark.parametrize("M,K", [(1, 336), (16, 336), (400, 336), (200, 4240)])
+def test_linear_infinite_scale_follows_the_sum(M, K):
+    """An infinite scale of a group whose integer sum is not zero gives an
+    infinity, in the row's first group (whatever pads K) and in its last."""
+    N, group = 40, 32
+    q, s_x = np.ones((M, K), np.int8), np.ones(M, np.float32)
+    packed = cuda(ref.pack(np.full((N, K), 3, np.int8), bwt.packed_ld(bwt.INT4, K)))
+    for at in (0, K // group):
+        s = torch.ones(N, bwt.gs_groups(K, group), device="cuda")
+        s[5, at] = float("inf")
+        y = bwt.lowbit_gs_linear(cuda(q), cuda(s_x), packed, s, group)
+        assert torch.isposinf(y[:, 5]).all()
+        y[:, 5] = 3 * K
+        assert (y == 3 * K).all()
 
 
 def test_linear_infinite_scale_stays_in_its_rows():
