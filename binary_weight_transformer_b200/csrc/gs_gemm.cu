@@ -532,6 +532,8 @@ gs_gemm_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant_
                 for (uint32_t i = 0; i < ST && i < g; ++i) {
                     const uint32_t gi = g - 1 - i;
                     drain_bar(&full_tma[gi % ST], (gi / ST) & 1u);
+                    // ... and so do the even CTA's arrivals for them
+                    if (ok) ok = wait_bar(&mma_done[gi % ST], (gi / ST) & 1u, abort_flag, a.status);
                 }
             }
         } else if (warp == 1) {

@@ -174,6 +174,57 @@ def test_linear_deep(M, K, N, group):
     check_linear(M, K, N, group, bwt.BF16, bwt.BF16, ldy=N + 7)
 
 
+@pytest.mark.parametrize("M", [1, 3, 40])
+@pytest.mark.parametrize("K,group", [(98304, 64), (98560, 32), (bwt.GS_MAX_K, 256)])
+def test_linear_longest_rows(M, K, group):
+    """K at and past what the single-token kernel keeps in shared memory, and
+    the largest.  Weights of -7 to 7 with 7s in every group pack to themselves."""
+    N = 9
+    gen = torch.Generator("cuda").manual_seed(K)
+    w = torch.randint(-7, 8, (N, K), device="cuda", generator=gen).float()
+    w[:, ::group] = 7
+    q = torch.randint(-128, 128, (M, K), device="cuda", generator=gen, dtype=torch.int8)
+    s_x = torch.rand(M, device="cuda", generator=gen) + 0.1
+    packed, s_g = bwt.lowbit_gs_pack(w, group)
+    assert (s_g == 1).all()
+    s_g *= torch.rand(s_g.shape, device="cuda", generator=gen) + 0.1
+    y = bwt.lowbit_gs_linear(q, s_x, packed, s_g, group)
+    acc = (q.double().view(M, 1, -1, group) * w.double().view(1, N, -1, group)).sum(-1) * s_g.double()
+    want, mag = acc.sum(-1) * s_x.double()[:, None], acc.abs().sum(-1) * s_x.double()[:, None]
+    bound = ref.linear_bound(want.cpu().numpy(), mag.cpu().numpy(), K // group, False)
+    assert (np.abs((y.double() - want).cpu().numpy()) <= bound).all()
+
+
+@pytest.mark.parametrize("M", [1, 5, 40, 200])
+def test_linear_rows_past_32_bits(M):
+    """Output rows so far apart that their offsets pass 2^31 elements."""
+    N, K = 40, 1280
+    ldy = 2 ** 31 // (M - 1) + 64 if M > 1 else N
+    packed, s_g = bwt.lowbit_gs_pack(cuda(weights(5, N, K)), 64)
+    q, s_x = (cuda(a) for a in tokens(6, M, K))
+    want = bwt.lowbit_gs_linear(q, s_x, packed, s_g, 64)
+    flat = torch.empty((M - 1) * ldy + N, device="cuda")
+    y = flat.as_strided((M, N), (ldy, 1))
+    bwt.lowbit_gs_linear(q, s_x, packed, s_g, 64, y=y)
+    assert torch.equal(y, want)
+
+
+def test_unpack_values_past_32_bits():
+    N, K = 70000, 32768  # 2.3e9 values
+    packed = torch.randint(0, 256, (N, K // 2), device="cuda", dtype=torch.uint8)
+    packed[(packed & 15) == 8] = 0x11
+    packed[(packed >> 4) == 8] = 0x11
+    s = torch.rand(N, K // 256, device="cuda") + 0.5
+    v = bwt.lowbit_gs_unpack(packed, s, K, 256, bwt.BF16)
+    for r in (0, N // 2, N - 1):
+        one = bwt.lowbit_gs_unpack(packed[r:r + 1], s[r:r + 1], K, 256, bwt.BF16)
+        assert torch.equal(v[r:r + 1], one)
+    again, s2 = bwt.lowbit_gs_pack(v, 256)
+    r = slice(N - 2, N)
+    p1, s1 = bwt.lowbit_gs_pack(v[r].contiguous(), 256)
+    assert torch.equal(again[r], p1) and torch.equal(s2[r], s1)
+
+
 @pytest.mark.parametrize("M", [1, 12, 200])
 def test_linear_strides(M):
     check_linear(M, 500, 50, 64, bwt.BF16, bwt.BF16, stable=True, lds=11, ldy=57, ldp=320)
@@ -282,6 +333,55 @@ def test_layer_in_a_graph_and_on_another_stream(M):
             got[i].append(bwt.lowbit_gs_linear(q, s_x, packed, s, 64, stream=st, y=torch.empty_like(want)))
     torch.cuda.synchronize()
     assert all(torch.equal(g, want) for half in got for g in half)
+
+
+@pytest.mark.parametrize("M,K,waits", [(300, 2560, True), (60, 9728, False), (200, 320, False), (128, 9728, True)])
+def test_timeout_is_reported_and_the_context_survives(M, K, waits):
+    """Every pipeline wait of the tcgen05 kernel is bounded: with the bound
+    lowered to one cycle the first wait that does not succeed at once gives up,
+    the status says so, and the kernel ends by itself; afterwards, with the
+    bound restored, the same call is right again.  (The two small
+    products run on the warp-level kernel, which has no such waits: estimated
+    9.4 + 0.33 * 6.8 * 4 = 18 against 4.2 + 2.6 + 0.7 + 19 * 0.67 = 20 us, and
+    4.7 + 0.33 * 0.22 * 13 = 5.6 against 4.2 + 0.7 + 3 * 0.67 = 6.9.)"""
+    N = 700
+    packed, s_g = bwt.lowbit_gs_pack(cuda(weights(5, N, K)), 64)
+    q, s_x = (cuda(a) for a in tokens(6, M, K))
+    want = bwt.lowbit_gs_linear(q, s_x, packed, s_g, 64)
+    torch.cuda.synchronize()
+    bwt.set_wait_limit(1)
+    try:
+        st = status_word()
+        y = bwt.lowbit_gs_linear(q, s_x, packed, s_g, 64, status=st)
+        torch.cuda.synchronize()
+        assert bwt.status_flags(st) == ([bwt.ERR_TIMEOUT] if waits else [])
+        assert waits or torch.equal(y, want)
+    finally:
+        bwt.set_wait_limit(0)
+    st = status_word()
+    assert torch.equal(bwt.lowbit_gs_linear(q, s_x, packed, s_g, 64, status=st), want)
+    assert st.item() == 0
+
+
+@pytest.mark.parametrize("M", [16, 100, 700])
+def test_two_products_at_once(M):
+    """Products of all kernels interleaved on three streams, each with operands
+    of its own."""
+    N, K, group = 520, 2560, 128
+    calls = []
+    for i in range(3):
+        packed, s_g = bwt.lowbit_gs_pack(cuda(weights(i, N, K)), group)
+        q, s_x = (cuda(a) for a in tokens(10 + i, M, K))
+        calls.append((q, s_x, packed, s_g, group))
+    want = [bwt.lowbit_gs_linear(*c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[torch.empty_like(want[0]) for _ in range(6)] for _ in calls]
+    for j in range(6):
+        for st, c, g in zip(streams, calls, got):
+            bwt.lowbit_gs_linear(*c, stream=st, y=g[j])
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for gs, w in zip(got, want) for g in gs)
 
 
 def test_wrappers_refuse_on_the_gpu():

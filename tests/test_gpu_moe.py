@@ -216,6 +216,20 @@ def test_experts_many_rows(counts, group):
     check_experts(counts, 1024, 257, group, bwt.F32, bwt.F32, spare=0)
 
 
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("E", [33, 300, bwt.MOE_MAX_EXPERTS])
+def test_many_experts(E, rows):
+    """As many experts as there may be, every third without rows."""
+    rng = np.random.default_rng(E)
+    check_experts([0 if e % 3 == 0 else int(rng.integers(rows, 2 * rows + 1)) for e in range(E)], 64, 24, 32, bwt.F32, bwt.F32)
+
+
+@pytest.mark.parametrize("rows", [3, 90])
+def test_one_expert_takes_all_rows(rows):
+    """The kernel is chosen for evenly spread rows; it is right for others."""
+    check_experts([0] * 20 + [20 * rows] + [0] * 11, 640, 72, 64, bwt.BF16, bwt.BF16)
+
+
 @pytest.mark.parametrize("counts", [[3, 0, 5], [150, 0, 260]])
 def test_experts_strides(counts):
     check_experts(counts, 500, 72, 64, bwt.BF16, bwt.F32, strided=True)
