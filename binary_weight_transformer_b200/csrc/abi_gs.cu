@@ -1,6 +1,8 @@
 // abi_gs.cu -- the C ABI of the group-scaled 4-bit layers and of the expert
 // routing: argument checks on the host, then kernel dispatch.  Every check
 // runs before any launch.  The operators are defined in include/lowbit.h.
+#include <cmath>
+
 #include <climits>
 
 #include "gs_internal.cuh"
@@ -56,21 +58,31 @@ lowbit_status check_slots(const void *pos, int64_t T, int k, int64_t rows)
     return aligned(pos, 4) ? LOWBIT_OK : LOWBIT_ERR_ALIGNMENT;
 }
 
-// The kernel for a call, by its estimated time in ns, measured on a B200 (512 to
-// 9728 features, 1 to 4096 tokens).  The warp-level kernel takes about 4.5 us,
-// 0.5 us per 1000 codes of K and, per million weights and pass of 16 tokens,
-// 0.21 us (groups of 128 and 256) or 0.33 us; gs_gemm_plan has the tcgen05
-// kernel's.  (Groups of 128, 64 tokens: 1280 -> 3584 takes 8.6 us on either,
-// 2560 -> 9728 27.5 and 14.9 us, 4096 -> 512 7.3 and 10.9 us.)  Experts are
-// taken to share the rows evenly; any distribution is correct on both.
+// The kernel for a call, by its estimated time in ns, measured on a B200 (26 to
+// 9728 features, 1 to 4096 tokens, up to 128 experts).  The warp-level kernel
+// takes about 4.5 us, 0.5 us per 1000 codes of K and, per million weights (rows
+// in steps of 32) and pass of 16 tokens, 0.21 us (groups of 128 and 256) or 0.33
+// us; gs_gemm_plan has the tcgen05 kernel's.  (Groups of 128, 64 tokens: 1280 ->
+// 3584 takes 8.6 us on either, 2560 -> 9728 27.5 and 14.9 us, 4096 -> 512 7.3 and
+// 10.9 us.)  Experts are taken to share the rows evenly, with half a pass more
+// each, 1.3 for the warp-level kernel's spread, and there 1.3 us for each pass
+// that a block does when an expert has twice its share: 16 experts of 1280 -> 3584
+// take 29 and 27 us at 17 rows each and 76 and 27 us at 64, 128 of 2048 -> 128
+// 16 and 26 us, 39 and 26 us.  Any distribution is correct on both.
 lowbit_status gs_product(const GsArgs &a, cudaStream_t st)
 {
     if (gs_gemv_takes(a)) return gs_gemv_launch(a, st);
     const int64_t active = a.offsets == nullptr ? 1 : a.E < a.M ? a.E : a.M;
-    const int64_t rows = (a.M + active - 1) / active;
-    if (rows <= 16) return gs_mma_launch(a, st);
-    const double pass = (a.gshift >= 7 ? 210.0 : 330.0) * 1e-6 * static_cast<double>(a.N) * static_cast<double>(a.K);
-    const double mma = 4500.0 + 0.5 * static_cast<double>(a.K) + pass * static_cast<double>(active * ((rows + 15) / 16));
+    if (a.M <= 16 * active) return gs_mma_launch(a, st);
+    const double rows = static_cast<double>(a.M) / static_cast<double>(active);
+    const double passes = a.offsets == nullptr ? static_cast<double>((a.M + 15) / 16) : 1.3 * (rows / 16.0 + 0.5);
+    const double pass = (a.gshift >= 7 ? 210.0 : 330.0) * 1e-6 * static_cast<double>((a.N + 31) / 32 * 32) *
+                        static_cast<double>(a.K);
+    double mma = 4500.0 + 0.5 * static_cast<double>(a.K) + pass * passes * static_cast<double>(active);
+    if (a.offsets != nullptr) {
+        const double chain = 3000.0 + 1300.0 * std::ceil(rows / 8.0 / static_cast<double>(gs_mma_lanes(a, 16)));
+        if (chain > mma) mma = chain;
+    }
     const GsGemmPlan p = gs_gemm_plan(a);
     return mma <= p.ns ? gs_mma_launch(a, st) : gs_gemm_launch(a, p, st);
 }

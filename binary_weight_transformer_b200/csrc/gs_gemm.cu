@@ -839,9 +839,11 @@ GsGemmPlan gs_gemm_plan(const GsArgs &a)
     for (int nt = 128; nt <= 256; nt *= 2) {
         const bool wide = nt == 256;
         const double drain = wide ? 100.0 + 480.0 * ends : 150.0 + 260.0 * ends, block = drain > 470.0 ? drain : 470.0;
-        // experts: an expert's last tile is half full on average
-        const int64_t active = a.E < a.M ? a.E : a.M, rows = a.M / active;
-        const int64_t tiles = wt * (a.offsets == nullptr ? (a.M + nt - 1) / nt : active * (1 + (rows - nt / 2 > 0 ? rows - nt / 2 : 0) / nt));
+        int64_t tiles = wt * ((a.M + nt - 1) / nt);
+        if (a.offsets != nullptr) {  // an expert's last tile is half full on average
+            const int64_t active = a.E < a.M ? a.E : a.M, most = a.M + active * (nt / 2) - 1;
+            tiles = wt * (most / nt > active ? most / nt : active);
+        }
         for (int split = 1; split <= 4; split *= 2) {
             const int64_t per = ((nkb + split - 1) / split + unit - 1) / unit * unit;
             if (split > 1 && (a.offsets != nullptr || per < 4 || (split - 1) * per >= nkb ||

@@ -79,6 +79,10 @@ __device__ __forceinline__ void divide(int64_t id, int64_t d, int64_t &quotient,
 bool gs_gemv_takes(const GsArgs &a);
 lowbit_status gs_gemv_launch(const GsArgs &a, cudaStream_t st);
 lowbit_status gs_mma_launch(const GsArgs &a, cudaStream_t st);
+// Blocks of that kernel that share an expert's passes of `tok` tokens: as many
+// as fill the SMs.  With one pass per expert on average, a larger expert's
+// follow one another.
+int64_t gs_mma_lanes(const GsArgs &a, int tok);
 // How the tcgen05 kernel would run a call: tokens per tile, pairs that share a
 // tile's K, K blocks of 128 for each, and the time that it is expected to take.
 struct GsGemmPlan {

@@ -134,6 +134,7 @@ struct Split {
     int per;      // runs of units per block of a cluster
     int chunk;    // units staged at once
     int split;    // blocks of a cluster
+    int lanes;    // experts: blocks along z that share an expert's passes
 };
 
 // TOK: tokens per pass, 8 or 16.  (Passes of 32 tokens, with 16 rows per warp,
@@ -173,10 +174,12 @@ gs_mma_kernel(const GsArgs a, const Split sp)
     const uint8_t *scales = static_cast<const uint8_t *>(a.s_g);
     const int s_size = a.s_bf16 ? 2 : 4;
     if (a.offsets != nullptr) {
-        gs_expert_rows(a.offsets, blockIdx.z, a.M, lo, hi, a.status);
-        packed += blockIdx.z * a.pstride;
-        scales += blockIdx.z * a.sstride * s_size;
-        step = TOK;
+        const unsigned e = blockIdx.z / static_cast<unsigned>(sp.lanes);
+        gs_expert_rows(a.offsets, static_cast<int>(e), a.M, lo, hi, a.status);
+        packed += e * a.pstride;
+        scales += e * a.sstride * s_size;
+        lo += static_cast<int64_t>(blockIdx.z % static_cast<unsigned>(sp.lanes)) * TOK;
+        step = static_cast<int64_t>(sp.lanes) * TOK;
     } else {
         lo = static_cast<int64_t>(blockIdx.z) * TOK;
         hi = a.M;
@@ -401,10 +404,11 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
     const int64_t units = (a.K + kUnit - 1) / kUnit;
     const int64_t runs = (units + kRun - 1) / kRun;
     const int64_t slabs = (a.N + kRows - 1) / kRows;
-    int64_t ztiles, active;
+    int64_t ztiles, active, lanes = 1;
     if (a.offsets != nullptr) {
-        ztiles = a.E;
-        active = a.E < a.M ? a.E : a.M;
+        lanes = gs_mma_lanes(a, TOK);
+        ztiles = a.E * lanes;
+        active = (a.E < a.M ? a.E : a.M) * lanes;
     } else {
         ztiles = (a.M + TOK - 1) / TOK;
         if (ztiles > 65535) ztiles = 65535;
@@ -439,7 +443,8 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
                                         static_cast<int>(bytes(max_chunk<TOK>(), kMaxKWarps))) == cudaSuccess ? 1 : 0;
         }) <= 0)
         return LOWBIT_ERR_CUDA;
-    const Split sp = {static_cast<int>(units), static_cast<int>(per), static_cast<int>(chunk), static_cast<int>(split)};
+    const Split sp = {static_cast<int>(units), static_cast<int>(per), static_cast<int>(chunk), static_cast<int>(split),
+                      static_cast<int>(lanes)};
     return launch_clusters_y(gs_mma_kernel<TOK, GM>,
                              dim3(static_cast<unsigned>(slabs), static_cast<unsigned>(split), static_cast<unsigned>(ztiles)),
                              dim3(static_cast<unsigned>(kRowWarps * kwarps * 32)), smem, st, static_cast<unsigned>(split), a,
@@ -458,6 +463,17 @@ lowbit_status launch_g(const GsArgs &a, cudaStream_t st)
 }
 
 }  // namespace gsm
+
+int64_t gs_mma_lanes(const GsArgs &a, int tok)
+{
+    const int64_t active = a.E < a.M ? a.E : a.M, passes = (a.M + active * tok - 1) / (active * tok);
+    if (passes < 2) return 1;
+    const int64_t slabs = (a.N + 8 * gsm::kRowWarps - 1) / (8 * gsm::kRowWarps);
+    int64_t lanes = device_sm_count() * 3 / (slabs * active);
+    if (lanes > 2 * passes) lanes = 2 * passes;
+    if (lanes * a.E > 65535) lanes = 65535 / a.E;
+    return lanes < 1 ? 1 : lanes;
+}
 
 lowbit_status gs_mma_launch(const GsArgs &a, cudaStream_t st)
 {
