@@ -47,10 +47,43 @@ __device__ __noinline__ int code_exact(float w, float s)
     return w < 0.0f ? -c : c;
 }
 
-template <bool BF16>
-__device__ __forceinline__ void load8(const void *w, int64_t at, int valid, bool vec, float (&v)[8])
+// A warp's 256 values in shared memory, eight per lane: 12 words apart, so
+// that both orders, eight consecutive per lane and 32 consecutive per access,
+// are free of bank conflicts.
+constexpr int kWarpStage = 32 * 12;
+__device__ __forceinline__ int stage_at(int e) { return (e >> 3) * 12 + (e & 7); }
+
+// Values [at, at + 8) of the lane, zeros past the first `valid`; the warp's 256
+// start at at - 8 lane.  Rows without the alignment for one access per lane
+// are loaded 32 consecutive values at a time and change places through shared
+// memory (eight loads 32 bytes apart took 2.5 times as long).
+template <bool BF16, bool VEC>
+__device__ __forceinline__ void load8(const void *w, int64_t at, int valid, float *stage, int lane, float (&v)[8])
 {
-    if (valid >= 8 && vec) {
+    if constexpr (!VEC) {
+        const int n = __shfl_sync(0xffffffffu, valid, 0);  // of the warp's first lane: all that is left of the row
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int e = i * 32 + lane;
+            const int64_t k = at - 8 * lane + e;
+            v[i] = 0.0f;
+            if (e < n) {
+                if constexpr (BF16) v[i] = __uint_as_float(ld_act_u16(static_cast<const uint16_t *>(w) + k));
+                else v[i] = ld_act_f32(static_cast<const float *>(w) + k);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            stage[stage_at(i * 32 + lane)] = BF16 ? __uint_as_float(__float_as_uint(v[i]) << 16) : v[i];
+        __syncwarp();
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float4 f = *reinterpret_cast<const float4 *>(stage + lane * 12 + 4 * h);
+            v[4 * h] = f.x, v[4 * h + 1] = f.y, v[4 * h + 2] = f.z, v[4 * h + 3] = f.w;
+        }
+        return;
+    }
+    if (valid >= 8) {
         if constexpr (BF16) {
             const uint4 u = ld_act_u4(static_cast<const uint16_t *>(w) + at);
 #pragma unroll
@@ -89,9 +122,37 @@ __device__ __forceinline__ float seventh(float a)
     return __fmaf_rn(__fmaf_rn(-7.0f, q, a), y, q);
 }
 
+// a * b + c on two values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
 // The packed word of a lane's eight weights, and (from the first lane of each
 // group of `lanes`) its scale.
-template <bool S16, int lanes>
+template <bool BF16, bool S16, int lanes>
 __device__ __forceinline__ uint32_t pack_word(const float (&v)[8], int lane, bool owns, void *s_at,
                                               int32_t *status)
 {
@@ -112,24 +173,46 @@ __device__ __forceinline__ uint32_t pack_word(const float (&v)[8], int lane, boo
     }
     if (s >= 0x1p-60f && s <= 0x1p+60f) {
         // u = RN(w * c), c within 2^-23 of 1/s (rcp.approx: 1 ulp), is within
-        // 7.03 * 1.5 * 2^-23 < 1.3e-6 of the exact quotient, so both round to
-        // the same integer unless u is that near a half; where one of eight
-        // weights is within 1e-5 (one lane in 10^4), all go by the definition.
-        // The rounding is the addition of 1.5 * 2^23, whose low bits are then
-        // the code in two's complement.  |u| <= 7.03: a bf16 scale is at most
-        // 2^-8 below the quotient, so no clip.
-        float c;
+        // 7.03 * 1.5 * 2^-23 < 1.3e-6 of the exact quotient.  |u| <= 7.03: a bf16
+        // scale is at most 2^-8 below the quotient, so no clip.  The rounding
+        // is the addition of 1.5 * 2^23, whose low bits are then the code in
+        // two's complement.
+        float c, m[8];
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(c) : "f"(s));
-        float m[8], far = 0.0f;
+        if constexpr (BF16) {
+            // A bf16 weight over its group's scale is often within u's error of
+            // a half h: for one in a few hundred w / (top / 7) (fp32 scale) or w
+            // / s (bf16 scale) IS h.  If it is not, it is at least 2.4e-4 away:
+            // with integers a, b of 8 bits, 14 a 2^p - (2k + 1) b 2^t (or 2 a 2^p -
+            // (2k + 1) b 2^t) is a multiple of 2^(t - 3) over 2 b 2^t.  So u is put
+            // on the grid of 2^-16, where the first kind is exactly h, and
+            // then moved by 2^-20 u to the side on which the fp32 scale's own
+            // rounding puts it; a bf16 scale, or an exact seventh, leaves the
+            // half, which goes to the even integer.
+            const float r = __fmaf_rn(-7.0f, s, __uint_as_float(top));
+            const float side = S16 || r == 0.0f ? 1.0f : r > 0.0f ? 1.0f + 0x1p-20f : 1.0f - 0x1p-20f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float u = __fmul_rn(v[i], c);
-            m[i] = __fadd_rn(u, 12582912.0f);
-            far = fmaxf(far, fabsf(__fsub_rn(u, __fsub_rn(m[i], 12582912.0f))));
-        }
-        if (far > 0.49999f) {
+            for (int i = 0; i < 8; i += 2) {
+                const float2 u = add2(mul2(make_float2(v[i], v[i + 1]), both(c)), both(192.0f));
+                const float2 f = fma2(add2(u, both(-192.0f)), both(side), both(12582912.0f));
+                m[i] = f.x, m[i + 1] = f.y;
+            }
+        } else {
+            // u and the quotient round to the same integer unless u is within
+            // 1e-5 of a half; where one of eight weights is (one lane in 10^4),
+            // all go by the definition.
+            float far = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[i] = __int_as_float(code_exact(v[i], s));
+            for (int i = 0; i < 8; i += 2) {
+                const float2 u = mul2(make_float2(v[i], v[i + 1]), both(c)), f = add2(u, both(12582912.0f));
+                const float2 d = fma2(add2(f, both(-12582912.0f)), both(-1.0f), u);
+                m[i] = f.x, m[i + 1] = f.y;
+                far = fmaxf(far, fmaxf(fabsf(d.x), fabsf(d.y)));
+            }
+            if (far > 0.49999f) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) m[i] = __int_as_float(code_exact(v[i], s));
+            }
         }
         // low bytes of four codes each, then their low nibbles side by side
         uint32_t four[2];
@@ -150,30 +233,48 @@ __device__ __forceinline__ uint32_t pack_word(const float (&v)[8], int lane, boo
     return word;
 }
 
-template <bool BF16, bool S16, int GS>
+// Quotients of numbers below 2^31 by a divisor d, by multiplication (Granlund
+// and Montgomery, PLDI 1994): with 2^(l - 1) < d <= 2^l and m = floor(2^(31 + l) / d)
+// + 1, n / d = floor(n m / 2^(31 + l)).
+struct Over {
+    uint32_t m = 0;
+    int shift = 0;
+    bool fits;  // all numbers are below 2^31
+    Over(uint32_t d, int64_t numbers) : fits(numbers <= INT32_MAX)
+    {
+        while ((uint64_t(1) << shift) < d) ++shift;
+        if (shift > 0) m = static_cast<uint32_t>((uint64_t(1) << (31 + shift)) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t quotient(uint32_t n) const { return shift > 0 ? __umulhi(n, m) >> (shift - 1) : n; }
+};
+
+// Block b takes unit b % units of the eight rows from 8 (b / units): with the
+// quotient by multiplication (`over`), the addresses are few instructions.
+template <bool BF16, bool S16, int GS, bool VEC>
 __global__ void __launch_bounds__(kThreads, 8)
-gs_pack_kernel(const void *__restrict__ w, int64_t N, int64_t K, int64_t ldw, int vec, int64_t units,
+gs_pack_kernel(const void *__restrict__ w, int64_t N, int64_t K, int64_t ldw, uint32_t units, Over over,
                uint8_t *__restrict__ packed, int64_t ldp, uint8_t *__restrict__ s_g, int64_t lds, int32_t *status)
 {
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
-    int64_t n, at;
-    divide(static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5), units, n, at);
+    __shared__ __align__(16) float stage[VEC ? 1 : kThreads / 32][VEC ? 4 : kWarpStage];
+    const uint32_t rows8 = over.quotient(blockIdx.x);
+    const int64_t n = static_cast<int64_t>(rows8) * (kThreads / 32) + (threadIdx.x >> 5);
     if (n >= N) return;
-    const int64_t k0 = at * kUnit + lane * 8;
-    const int64_t left = K - k0;
+    const int k0 = static_cast<int>(blockIdx.x - rows8 * units) * kUnit + lane * 8;
+    const int left = static_cast<int>(K) - k0;
     float v[8];
-    load8<BF16>(w, n * ldw + k0, left >= 8 ? 8 : left > 0 ? static_cast<int>(left) : 0, vec != 0, v);
-    const uint32_t word = pack_word<S16, (1 << GS) / 8>(v, lane, left > 0, s_g + (n * lds + (k0 >> GS)) * (S16 ? 2 : 4), status);
+    load8<BF16, VEC>(w, n * ldw + k0, left, stage[VEC ? 0 : threadIdx.x >> 5], lane, v);
+    const uint32_t word = pack_word<BF16, S16, (1 << GS) / 8>(v, lane, left > 0, s_g + (n * lds + (k0 >> GS)) * (S16 ? 2 : 4), status);
     if (k0 / 2 < ldp) *reinterpret_cast<uint32_t *>(packed + n * ldp + k0 / 2) = word;
 }
 
-template <bool BF16, int U>
+template <bool BF16, int U, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 gs_unpack_kernel(const uint8_t *__restrict__ packed, int64_t ldp, const void *__restrict__ s_g, int s_bf16,
-                 int64_t lds, int64_t N, int64_t K, int gshift, int64_t words, void *__restrict__ w, int64_t ldw,
-                 int vec, int32_t *status)
+                 int64_t lds, int64_t N, int64_t K, int gshift, int64_t words, Over over, void *__restrict__ w, int64_t ldw,
+                 int32_t *status)
 {
     pdl_wait();
     pdl_trigger();
@@ -183,7 +284,13 @@ gs_unpack_kernel(const uint8_t *__restrict__ packed, int64_t ldp, const void *__
     for (int u = 0; u < U; ++u) {
         const int64_t idx = (static_cast<int64_t>(blockIdx.x) * U + u) * kThreads + threadIdx.x;
         int64_t wi;
-        divide(idx, words, row[u], wi);
+        if (over.fits) {
+            row[u] = over.quotient(static_cast<uint32_t>(idx));
+            wi = static_cast<uint32_t>(idx) - static_cast<uint32_t>(row[u]) * static_cast<uint32_t>(words);
+        } else {
+            row[u] = idx / words;
+            wi = idx % words;
+        }
         k0s[u] = wi * 8;
         word[u] = scale[u] = 0;
         if (row[u] < N) {
@@ -193,13 +300,16 @@ gs_unpack_kernel(const uint8_t *__restrict__ packed, int64_t ldp, const void *__
             else scale[u] = ld_act_u32(static_cast<const float *>(s_g) + at);
         }
     }
+    __shared__ __align__(16) float stages[VEC ? 1 : kThreads / 32][VEC ? 4 : kWarpStage];
+    float *stage = stages[VEC ? 0 : threadIdx.x >> 5];
+    const int lane = threadIdx.x & 31;
     bool bad = false;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        if (row[u] >= N) break;
+        if (VEC && row[u] >= N) break;
         const float s = __uint_as_float(s_bf16 ? scale[u] << 16 : scale[u]);
         const int64_t n = row[u], k0 = k0s[u];
-        const int valid = K - k0 >= 8 ? 8 : static_cast<int>(K - k0);
+        const int valid = n >= N ? 0 : K - k0 >= 8 ? 8 : static_cast<int>(K - k0);
         // bits no code of the row owns, and reserved fields: a nibble 1000 is a
         // zero nibble of x, which the subtraction's borrow marks
         uint32_t codes = word[u];
@@ -214,11 +324,60 @@ gs_unpack_kernel(const uint8_t *__restrict__ packed, int64_t ldp, const void *__
                 }
             }
         }
+        // a nibble c + 8 in the low bits of 2^23 is 2^23 + 8 + c
         float v[8];
+        const uint32_t shifted = codes ^ 0x88888888u, half[2] = {shifted & 0x0f0f0f0fu, (shifted >> 4) & 0x0f0f0f0fu};
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            v[i] = __fmul_rn(static_cast<float>(static_cast<int>(codes << (28 - 8 * (i & 3) - 4 * (i >> 2))) >> 28), s);
-        if (valid == 8 && vec) {
+        for (int i = 0; i < 8; i += 2) {
+            const float2 f = make_float2(__uint_as_float(__byte_perm(half[i >> 2], 0x4b000000u, 0x7650 + (i & 3))),
+                                         __uint_as_float(__byte_perm(half[i >> 2], 0x4b000000u, 0x7651 + (i & 3))));
+            const float2 o = mul2(add2(f, both(-8388616.0f)), both(s));
+            v[i] = o.x, v[i + 1] = o.y;
+        }
+        if constexpr (!VEC) {
+            // 32 consecutive values per store (eight stores 32 bytes apart
+            // took 3 times as long)
+            *reinterpret_cast<float4 *>(stage + lane * 12) = make_float4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<float4 *>(stage + lane * 12 + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            __syncwarp();
+            const int64_t mine = n * ldw + k0, first = __shfl_sync(0xffffffffu, mine, 0);
+            if (__all_sync(0xffffffffu, valid == 8 && mine == first + 8 * lane)) {
+                if constexpr (BF16) {
+                    // pairs from the first 4-byte boundary on
+                    __nv_bfloat16 *dst = static_cast<__nv_bfloat16 *>(w) + first;
+                    const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(dst) >> 1) & 1;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int e = odd + 2 * (lane + 32 * i);
+                        const float lo = stage[stage_at(e < 256 ? e : 0)], hi = stage[stage_at(e + 1 < 256 ? e + 1 : 0)];
+                        if (e + 1 < 256) {
+                            const __nv_bfloat162 o = __floats2bfloat162_rn(lo, hi);
+                            *reinterpret_cast<__nv_bfloat162 *>(dst + e) = o;
+                        } else {  // the last value, and the first
+                            dst[255] = __float2bfloat16_rn(lo);
+                            dst[0] = __float2bfloat16_rn(hi);
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        static_cast<float *>(w)[first + i * 32 + lane] = stage[stage_at(i * 32 + lane)];
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int from = i * 4 + (lane >> 3), e = lane & 7;  // value e of lane `from`
+                    const int64_t at = __shfl_sync(0xffffffffu, mine, from) + e;
+                    const int left = __shfl_sync(0xffffffffu, valid, from);
+                    const float f = stage[stage_at(i * 32 + lane)];
+                    if (e < left) {
+                        if constexpr (BF16) static_cast<__nv_bfloat16 *>(w)[at] = __float2bfloat16_rn(f);
+                        else static_cast<float *>(w)[at] = f;
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (valid == 8) {
             if constexpr (BF16) {
                 uint4 o;
 #pragma unroll
@@ -251,11 +410,18 @@ bool rows_aligned(const void *p, int64_t ld, int64_t esz)
     return reinterpret_cast<uintptr_t>(p) % (8 * esz) == 0 && ld % 8 == 0;
 }
 
+template <bool BF16>
+auto unpack_kernel(bool many, bool vec)
+{
+    if (vec) return many ? gs_unpack_kernel<BF16, kInFlight, true> : gs_unpack_kernel<BF16, 1, true>;
+    return many ? gs_unpack_kernel<BF16, kInFlight, false> : gs_unpack_kernel<BF16, 1, false>;
+}
+
 struct PackArgs {
     const void *w;
     int64_t N, K, ldw;
     int vec;
-    int64_t units;
+    uint32_t units;
     uint8_t *packed;
     int64_t ldp;
     uint8_t *s_g;
@@ -268,8 +434,9 @@ struct PackArgs {
 template <bool BF16, bool S16, int GS>
 lowbit_status pack_one(const PackArgs &a)
 {
-    return launch_pdl(gs_pack_kernel<BF16, S16, GS>, dim3(a.blocks), dim3(kThreads), 0, a.st, 0, a.w, a.N, a.K, a.ldw,
-                      a.vec, a.units, a.packed, a.ldp, a.s_g, a.lds, a.status);
+    return launch_pdl(a.vec ? gs_pack_kernel<BF16, S16, GS, true> : gs_pack_kernel<BF16, S16, GS, false>, dim3(a.blocks),
+                      dim3(kThreads), 0, a.st, 0, a.w, a.N, a.K, a.ldw, a.units, Over(a.units, a.blocks), a.packed, a.ldp, a.s_g, a.lds,
+                      a.status);
 }
 
 template <bool BF16, bool S16>
@@ -289,9 +456,9 @@ lowbit_status gs_pack_launch(const void *w, int w_bf16, int64_t N, int64_t K, in
                              int64_t ldp, void *s_g, int s_bf16, int64_t lds, int32_t *status, cudaStream_t st)
 {
     const int64_t units = (ldp * 2 + kUnit - 1) / kUnit;
-    const int64_t blocks = (N * units + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
-    const PackArgs a = {w, N, K, ldw, rows_aligned(w, ldw, w_bf16 ? 2 : 4) ? 1 : 0, units, packed, ldp,
+    const int64_t blocks = (N + kThreads / 32 - 1) / (kThreads / 32) * units;
+    if (blocks > INT32_MAX || units > INT32_MAX / kUnit) return LOWBIT_ERR_UNSUPPORTED;
+    const PackArgs a = {w, N, K, ldw, rows_aligned(w, ldw, w_bf16 ? 2 : 4) ? 1 : 0, static_cast<uint32_t>(units), packed, ldp,
                         static_cast<uint8_t *>(s_g), lds, status, static_cast<unsigned>(blocks), st};
     return w_bf16 ? (s_bf16 ? pack_groups<true, true>(a, gshift) : pack_groups<true, false>(a, gshift))
                   : (s_bf16 ? pack_groups<false, true>(a, gshift) : pack_groups<false, false>(a, gshift));
@@ -302,16 +469,15 @@ lowbit_status gs_unpack_launch(const uint8_t *packed, int64_t ldp, const void *s
                                cudaStream_t st)
 {
     const int64_t words = (K + 7) / 8;
-    // several words per thread once that still fills the GPU
+    // several words per thread once that still fills the G1
     const bool many = N * words >= static_cast<int64_t>(device_sm_count()) * 2048 * kInFlight;
     const int64_t per_block = kThreads * (many ? kInFlight : 1);
     const int64_t blocks = (N * words + per_block - 1) / per_block;
     if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
-    const int vec = rows_aligned(w, ldw, w_bf16 ? 2 : 4) ? 1 : 0;
-    auto kernel = w_bf16 ? (many ? gs_unpack_kernel<true, kInFlight> : gs_unpack_kernel<true, 1>)
-                         : (many ? gs_unpack_kernel<false, kInFlight> : gs_unpack_kernel<false, 1>);
+    const bool vec = rows_aligned(w, ldw, w_bf16 ? 2 : 4);
+    auto kernel = w_bf16 ? unpack_kernel<true>(many, vec) : unpack_kernel<false>(many, vec);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, 0, packed, ldp, s_g, s_bf16, lds,
-                      N, K, gshift, words, w, ldw, vec, status);
+                      N, K, gshift, words, Over(static_cast<uint32_t>(words), blocks * per_block), w, ldw, status);
 }
 
 }  // namespace lowbit
