@@ -10,6 +10,8 @@
 // combine and backward run by token, which reads a token's row (x, dy) once
 // for its k slots instead of once per slot, and needs only pos.  No atomics
 // on data: every output value has one writer and a fixed order of additions.
+#include <type_traits>
+
 #include "gs_internal.cuh"
 #include "tc_common.cuh"
 
@@ -181,10 +183,18 @@ moe_plan_kernel(const void *__restrict__ experts, int64_t slots, int E, int C, i
 // ---------------------------------------------------------------------------
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kVecs = 4;  // vectors per lane and row piece
+
+// Vectors per lane and row piece.
+template <typename V> __host__ __device__ constexpr int pieces_of() { return sizeof(V) == 16 ? 4 : 8; }
 
 template <typename V> __device__ __forceinline__ V load_vec(const V *p);
 template <> __device__ __forceinline__ uint4 load_vec(const uint4 *p) { return ld_act_u4(p); }
+template <> __device__ __forceinline__ uint2 load_vec(const uint2 *p)
+{
+    uint2 v;
+    asm volatile("ld.global.cg.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+    return v;
+}
 template <> __device__ __forceinline__ uint32_t load_vec(const uint32_t *p) { return ld_act_u32(p); }
 template <> __device__ __forceinline__ uint16_t load_vec(const uint16_t *p) { return ld_act_u16(p); }
 template <> __device__ __forceinline__ uint8_t load_vec(const uint8_t *p)
@@ -214,7 +224,7 @@ __device__ __forceinline__ void slot_rows(const int32_t *pos, int64_t s, int n, 
 
 constexpr int kBatch = 4;  // slots taken together
 
-// A warp copies one piece (32 lanes x kVecs vectors) of a token's row to the
+// A warp copies one piece (32 lanes x kMine vectors) of a token's row to the
 // rows of its k slots.
 template <typename V>
 __global__ void __launch_bounds__(kThreads)
@@ -222,6 +232,7 @@ moe_gather_kernel(const uint8_t *__restrict__ x, int64_t nvec, int64_t pieces, i
                   const int32_t *__restrict__ pos, int64_t T, int k, uint8_t *__restrict__ out, int64_t ldo,
                   float *__restrict__ s_out, int64_t rows, int32_t *status)
 {
+    constexpr int kMine = pieces_of<V>();
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
@@ -230,10 +241,10 @@ moe_gather_kernel(const uint8_t *__restrict__ x, int64_t nvec, int64_t pieces, i
     divide(id, pieces, t, piece);
     if (t >= T) return;
     const V *src = reinterpret_cast<const V *>(x + t * ldx);
-    const int64_t v0 = piece * (32 * kVecs) + lane;
-    V v[kVecs];
+    const int64_t v0 = piece * (32 * kMine) + lane;
+    V v[kMine];
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i)
+    for (int i = 0; i < kMine; ++i)
         if (v0 + 32 * i < nvec) v[i] = load_vec(src + v0 + 32 * i);
     const float s = s_x != nullptr && piece == 0 ? ld_act_f32(s_x + t) : 0.0f;
     for (int j0 = 0; j0 < k; j0 += kBatch) {
@@ -244,7 +255,7 @@ moe_gather_kernel(const uint8_t *__restrict__ x, int64_t nvec, int64_t pieces, i
             if (p[b] < 0) continue;
             V *dst = reinterpret_cast<V *>(out + p[b] * ldo);
 #pragma unroll
-            for (int i = 0; i < kVecs; ++i)
+            for (int i = 0; i < kMine; ++i)
                 if (v0 + 32 * i < nvec) dst[v0 + 32 * i] = v[i];
             if (s_x != nullptr && piece == 0 && lane == 0) s_out[p[b]] = s;
         }
@@ -254,83 +265,66 @@ moe_gather_kernel(const uint8_t *__restrict__ x, int64_t nvec, int64_t pieces, i
 // ---------------------------------------------------------------------------
 // combine and its gradient
 // ---------------------------------------------------------------------------
-// kN values per vector, in fp32 registers.
-template <bool BF16, bool VEC> struct Row;
-template <> struct Row<true, true> {
-    static constexpr int kN = 8;
-    using Raw = uint4;
-    static __device__ __forceinline__ Raw load(const void *p, int64_t at)
+// Vectors of BYTES bytes: kN values, in fp32 registers.  16 bytes where rows
+// allow it; below that the next that they do (K = 1002 in bf16: 4), with as
+// many more vectors in flight.
+template <bool BF16, int BYTES>
+struct Row {
+    static constexpr int kN = BYTES / (BF16 ? 2 : 4);
+    static constexpr int kFlight = BYTES == 16 ? 1 : BYTES == 8 ? 2 : 4;  // times the vectors of 16 bytes
+    using Raw = std::conditional_t<BYTES == 16, uint4, std::conditional_t<BYTES == 8, uint2, std::conditional_t<BYTES == 4, uint32_t, uint16_t>>>;
+    static __device__ __forceinline__ Raw *at(void *p, int64_t i) { return reinterpret_cast<Raw *>(static_cast<uint8_t *>(p) + i * (BF16 ? 2 : 4)); }
+    static __device__ __forceinline__ Raw load(const void *p, int64_t i)
     {
-        return ld_act_u4(static_cast<const uint16_t *>(p) + at);
+        return load_vec(reinterpret_cast<const Raw *>(static_cast<const uint8_t *>(p) + i * (BF16 ? 2 : 4)));
+    }
+    static __device__ __forceinline__ uint32_t word(const Raw &r, int i)
+    {
+        if constexpr (BYTES > 4) return (&r.x)[i];
+        else return r;
     }
     static __device__ __forceinline__ float get(const Raw &r, int i)
     {
-        const uint32_t w = (&r.x)[i >> 1];
-        return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+        if constexpr (!BF16) return __uint_as_float(word(r, i));
+        else return __uint_as_float((i & 1) ? (word(r, i >> 1) & 0xffff0000u) : (word(r, i >> 1) << 16));
     }
-    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&v)[kN])
+    static __device__ __forceinline__ void store(void *p, int64_t i, const float (&v)[kN])
     {
-        uint4 u;
+        Raw r;
+        if constexpr (BF16 && kN == 1) {
+            r = __bfloat16_as_ushort(__float2bfloat16_rn(v[0]));
+        } else {
+            uint32_t w[BYTES / 4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-            (&u.x)[i] = *reinterpret_cast<const uint32_t *>(&b);
+            for (int j = 0; j < BYTES / 4; ++j) {
+                if constexpr (BF16) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+                    w[j] = *reinterpret_cast<const uint32_t *>(&b);
+                } else {
+                    w[j] = __float_as_uint(v[j]);
+                }
+            }
+            if constexpr (BYTES == 4) r = w[0];
+            else if constexpr (BYTES == 8) r = make_uint2(w[0], w[1]);
+            else r = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + at) = u;
-    }
-};
-template <> struct Row<false, true> {
-    static constexpr int kN = 4;
-    using Raw = uint4;
-    static __device__ __forceinline__ Raw load(const void *p, int64_t at)
-    {
-        return ld_act_u4(static_cast<const float *>(p) + at);
-    }
-    static __device__ __forceinline__ float get(const Raw &r, int i) { return __uint_as_float((&r.x)[i]); }
-    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&v)[kN])
-    {
-        *reinterpret_cast<float4 *>(static_cast<float *>(p) + at) = make_float4(v[0], v[1], v[2], v[3]);
-    }
-};
-template <> struct Row<true, false> {
-    static constexpr int kN = 1;
-    using Raw = uint16_t;
-    static __device__ __forceinline__ Raw load(const void *p, int64_t at)
-    {
-        return ld_act_u16(static_cast<const uint16_t *>(p) + at);
-    }
-    static __device__ __forceinline__ float get(const Raw &r, int) { return __uint_as_float(static_cast<uint32_t>(r) << 16); }
-    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&v)[kN])
-    {
-        static_cast<__nv_bfloat16 *>(p)[at] = __float2bfloat16_rn(v[0]);
-    }
-};
-template <> struct Row<false, false> {
-    static constexpr int kN = 1;
-    using Raw = float;
-    static __device__ __forceinline__ Raw load(const void *p, int64_t at)
-    {
-        return ld_act_f32(static_cast<const float *>(p) + at);
-    }
-    static __device__ __forceinline__ float get(const Raw &r, int) { return r; }
-    static __device__ __forceinline__ void store(void *p, int64_t at, const float (&v)[kN])
-    {
-        static_cast<float *>(p)[at] = v[0];
+        *at(p, i) = r;
     }
 };
 
-constexpr int kCombineVecs = 2;  // vectors per lane and row piece
+constexpr int kCombineVecs = 2;  // vectors of 16 bytes per lane and row piece
 
 // A warp adds `per` consecutive pieces of a token's rows: the slots and
 // weights, which the rows' addresses wait for, are then read once for several
 // pieces.
-template <bool BF16, bool VEC>
+template <bool BF16, int BYTES>
 __global__ void __launch_bounds__(kThreads)
 moe_combine_kernel(const void *__restrict__ ys, int64_t ldys, int64_t rows, const int32_t *__restrict__ pos,
                    const float *__restrict__ weights, int64_t T, int k, int64_t nvec, int64_t warps_per_row, int per,
                    void *__restrict__ y, int64_t ldy, int32_t *status)
 {
-    using R = Row<BF16, VEC>;
+    using R = Row<BF16, BYTES>;
+    constexpr int kMine = kCombineVecs * R::kFlight;
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31;
@@ -338,7 +332,7 @@ moe_combine_kernel(const void *__restrict__ ys, int64_t ldys, int64_t rows, cons
     int64_t t, part;
     divide(id, warps_per_row, t, part);
     if (t >= T) return;
-    int64_t v0 = part * (32 * kCombineVecs) * per + lane;
+    int64_t v0 = part * (32 * kMine) * per + lane;
     int32_t p[kBatch];
     float w[kBatch];
     auto slots = [&](int j0) {
@@ -347,25 +341,25 @@ moe_combine_kernel(const void *__restrict__ ys, int64_t ldys, int64_t rows, cons
         slot_rows(pos, t * k + j0, k - j0, rows, status, p);
     };
     slots(0);
-    for (int i0 = 0; i0 < per && v0 - lane < nvec; ++i0, v0 += 32 * kCombineVecs) {
-        float acc[kCombineVecs][R::kN];
+    for (int i0 = 0; i0 < per && v0 - lane < nvec; ++i0, v0 += 32 * kMine) {
+        float acc[kMine][R::kN];
 #pragma unroll
-        for (int i = 0; i < kCombineVecs; ++i)
+        for (int i = 0; i < kMine; ++i)
 #pragma unroll
             for (int c = 0; c < R::kN; ++c) acc[i][c] = 0.0f;
         for (int j0 = 0; j0 < k; j0 += kBatch) {
             if (k > kBatch && (j0 != 0 || i0 != 0)) slots(j0);
-            typename R::Raw raw[kBatch][kCombineVecs];
+            typename R::Raw raw[kBatch][kMine];
 #pragma unroll
             for (int b = 0; b < kBatch; ++b)
 #pragma unroll
-                for (int i = 0; i < kCombineVecs; ++i)
+                for (int i = 0; i < kMine; ++i)
                     if (p[b] >= 0 && v0 + 32 * i < nvec) raw[b][i] = R::load(ys, p[b] * ldys + (v0 + 32 * i) * R::kN);
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
                 if (p[b] < 0) continue;
 #pragma unroll
-                for (int i = 0; i < kCombineVecs; ++i)
+                for (int i = 0; i < kMine; ++i)
                     if (v0 + 32 * i < nvec) {
 #pragma unroll
                         for (int c = 0; c < R::kN; ++c) acc[i][c] = __fmaf_rn(w[b], R::get(raw[b][i], c), acc[i][c]);
@@ -373,7 +367,7 @@ moe_combine_kernel(const void *__restrict__ ys, int64_t ldys, int64_t rows, cons
             }
         }
 #pragma unroll
-        for (int i = 0; i < kCombineVecs; ++i)
+        for (int i = 0; i < kMine; ++i)
             if (v0 + 32 * i < nvec) R::store(y, t * ldy + (v0 + 32 * i) * R::kN, acc[i]);
     }
 }
@@ -382,14 +376,15 @@ moe_combine_kernel(const void *__restrict__ ys, int64_t ldys, int64_t rows, cons
 // vectors lane + 32 * (warp + W * i) of the rows, kBatch slots at a time; a
 // slot's partial dots are summed over the lanes by shuffles and over the W
 // warps through shared memory, in a fixed order.
-template <bool BF16, bool VEC>
+template <bool BF16, int BYTES>
 __global__ void __launch_bounds__(kThreads)
 moe_combine_backward_kernel(const void *__restrict__ dy, int64_t lddy, const void *__restrict__ ys, int64_t ldys,
                             int64_t rows, const int32_t *__restrict__ pos, const float *__restrict__ weights,
                             int64_t T, int k, int64_t nvec, int W, void *__restrict__ d_ys, int64_t ldd,
                             float *__restrict__ d_w, int32_t *status)
 {
-    using R = Row<BF16, VEC>;
+    using R = Row<BF16, BYTES>;
+    constexpr int kMine = R::kFlight;
     __shared__ float part[kWarps][kBatch];
     pdl_wait();
     pdl_trigger();
@@ -406,23 +401,32 @@ moe_combine_backward_kernel(const void *__restrict__ dy, int64_t lddy, const voi
         }
         slot_rows(pos, t * k + j0, t < T ? k - j0 : 0, rows, status, p);
         if (t < T) {
-            for (int64_t v = lane + 32 * wt; v < nvec; v += 32 * W) {
-                const typename R::Raw g = R::load(dy, t * lddy + v * R::kN);
-                typename R::Raw raw[kBatch];
+            // kMine vectors of each row at a time
+            for (int64_t v0 = lane + 32 * wt; v0 < nvec; v0 += 32 * W * kMine) {
+                typename R::Raw g[kMine], raw[kBatch][kMine];
+#pragma unroll
+                for (int i = 0; i < kMine; ++i)
+                    if (v0 + 32 * W * i < nvec) g[i] = R::load(dy, t * lddy + (v0 + 32 * W * i) * R::kN);
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b)
-                    if (p[b] >= 0) raw[b] = R::load(ys, p[b] * ldys + v * R::kN);
+#pragma unroll
+                    for (int i = 0; i < kMine; ++i)
+                        if (p[b] >= 0 && v0 + 32 * W * i < nvec) raw[b][i] = R::load(ys, p[b] * ldys + (v0 + 32 * W * i) * R::kN);
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
                     if (p[b] < 0) continue;
-                    float o[R::kN];
 #pragma unroll
-                    for (int c = 0; c < R::kN; ++c) {
-                        const float gc = R::get(g, c);
-                        dot[b] = __fmaf_rn(gc, R::get(raw[b], c), dot[b]);
-                        o[c] = __fmul_rn(w[b], gc);
+                    for (int i = 0; i < kMine; ++i) {
+                        if (v0 + 32 * W * i >= nvec) break;
+                        float o[R::kN];
+#pragma unroll
+                        for (int c = 0; c < R::kN; ++c) {
+                            const float gc = R::get(g[i], c);
+                            dot[b] = __fmaf_rn(gc, R::get(raw[b][i], c), dot[b]);
+                            o[c] = __fmul_rn(w[b], gc);
+                        }
+                        R::store(d_ys, p[b] * ldd + (v0 + 32 * W * i) * R::kN, o);
                     }
-                    R::store(d_ys, p[b] * ldd + v * R::kN, o);
                 }
             }
         }
@@ -442,10 +446,13 @@ moe_combine_backward_kernel(const void *__restrict__ dy, int64_t lddy, const voi
     }
 }
 
-bool multiple_of(int64_t v, const void *a, int64_t la, const void *b, int64_t lb, int64_t n)
+// The widest access, 16 bytes or less, that addresses, row strides and row
+// length (bytes) allow.
+int64_t widest(const void *a, int64_t la, const void *b, int64_t lb, int64_t n)
 {
-    return (reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | static_cast<uint64_t>(la) |
-            static_cast<uint64_t>(lb) | static_cast<uint64_t>(n)) % static_cast<uint64_t>(v) == 0;
+    const uint64_t bits = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | static_cast<uint64_t>(la) |
+                          static_cast<uint64_t>(lb) | static_cast<uint64_t>(n) | 16u;
+    return static_cast<int64_t>(bits & (~bits + 1));
 }
 
 }  // namespace
@@ -486,15 +493,14 @@ lowbit_status moe_gather_launch(const void *x, int64_t row_bytes, int64_t ldx_by
                                 const int32_t *pos, int64_t T, int k, void *out, int64_t ldo_bytes, float *s_out,
                                 int64_t rows, int32_t *status, cudaStream_t st)
 {
-    int64_t v = 16;
-    if (!multiple_of(16, x, ldx_bytes, out, ldo_bytes, row_bytes)) v = 4;
-    if (v == 4 && !multiple_of(4, x, ldx_bytes, out, ldo_bytes, row_bytes)) v = 2;
-    if (v == 2 && !multiple_of(2, x, ldx_bytes, out, ldo_bytes, row_bytes)) v = 1;
+    const int64_t v = widest(x, ldx_bytes, out, ldo_bytes, row_bytes);
     const int64_t nvec = row_bytes / v;
-    const int64_t pieces = (nvec + 32 * kVecs - 1) / (32 * kVecs);
+    const int64_t each = 32 * (v == 16 ? pieces_of<uint4>() : pieces_of<uint2>());
+    const int64_t pieces = (nvec + each - 1) / each;
     const int64_t blocks = (T * pieces + kWarps - 1) / kWarps;
     if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
     auto kernel = v == 16  ? moe_gather_kernel<uint4>
+                  : v == 8 ? moe_gather_kernel<uint2>
                   : v == 4 ? moe_gather_kernel<uint32_t>
                   : v == 2 ? moe_gather_kernel<uint16_t>
                            : moe_gather_kernel<uint8_t>;
@@ -508,9 +514,10 @@ lowbit_status moe_combine_launch(const void *ys, int bf16, int64_t ldys, int64_t
                                  int32_t *status, cudaStream_t st)
 {
     const int64_t esz = bf16 ? 2 : 4;
-    const bool vec = multiple_of(16, ys, ldys * esz, y, ldy * esz, K * esz);
-    const int64_t nvec = vec ? K * esz / 16 : K;
-    const int64_t pieces = (nvec + 32 * kCombineVecs - 1) / (32 * kCombineVecs);
+    const int64_t v = widest(ys, ldys * esz, y, ldy * esz, K * esz);
+    const int64_t nvec = K * esz / v;
+    const int64_t each = 32 * kCombineVecs * (v == 16 ? 1 : v == 8 ? 2 : 4);
+    const int64_t pieces = (nvec + each - 1) / each;
     // Pieces per warp: as many as leave about 32 warps for every SM.
     int64_t per = T * pieces / (static_cast<int64_t>(device_sm_count()) * 32);
     if (per > pieces) per = pieces;
@@ -519,8 +526,13 @@ lowbit_status moe_combine_launch(const void *ys, int bf16, int64_t ldys, int64_t
     const int64_t warps = (pieces + per - 1) / per;
     const int64_t blocks = (T * warps + kWarps - 1) / kWarps;
     if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
-    auto kernel = bf16 ? (vec ? moe_combine_kernel<true, true> : moe_combine_kernel<true, false>)
-                       : (vec ? moe_combine_kernel<false, true> : moe_combine_kernel<false, false>);
+    auto kernel = bf16 ? (v == 16  ? moe_combine_kernel<true, 16>
+                          : v == 8 ? moe_combine_kernel<true, 8>
+                          : v == 4 ? moe_combine_kernel<true, 4>
+                                   : moe_combine_kernel<true, 2>)
+                       : (v == 16  ? moe_combine_kernel<false, 16>
+                          : v == 8 ? moe_combine_kernel<false, 8>
+                                   : moe_combine_kernel<false, 4>);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, 0, ys, ldys, rows, pos,
                       weights, T, k, nvec, warps, static_cast<int>(per), y, ldy, status);
 }
@@ -531,9 +543,9 @@ lowbit_status moe_combine_backward_launch(const void *dy, int64_t lddy, const vo
                                           cudaStream_t st)
 {
     const int64_t esz = bf16 ? 2 : 4;
-    const bool vec = multiple_of(16, dy, lddy * esz, ys, ldys * esz, K * esz) &&
-                     multiple_of(16, d_ys, ldd * esz, d_ys, ldd * esz, 0);
-    const int64_t nvec = vec ? K * esz / 16 : K;
+    const int64_t v1 = widest(dy, lddy * esz, ys, ldys * esz, K * esz), v2 = widest(d_ys, ldd * esz, d_ys, 0, 0);
+    const int64_t v = v1 < v2 ? v1 : v2;
+    const int64_t nvec = K * esz / v;
     // Warps per token: enough for about 16 warps on every SM, and no more
     // than the row has 32-vector pieces.
     int W = 1;
@@ -541,8 +553,13 @@ lowbit_status moe_combine_backward_launch(const void *dy, int64_t lddy, const vo
     const int64_t per = kWarps / W;
     const int64_t blocks = (T + per - 1) / per;
     if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
-    auto kernel = bf16 ? (vec ? moe_combine_backward_kernel<true, true> : moe_combine_backward_kernel<true, false>)
-                       : (vec ? moe_combine_backward_kernel<false, true> : moe_combine_backward_kernel<false, false>);
+    auto kernel = bf16 ? (v == 16  ? moe_combine_backward_kernel<true, 16>
+                          : v == 8 ? moe_combine_backward_kernel<true, 8>
+                          : v == 4 ? moe_combine_backward_kernel<true, 4>
+                                   : moe_combine_backward_kernel<true, 2>)
+                       : (v == 16  ? moe_combine_backward_kernel<false, 16>
+                          : v == 8 ? moe_combine_backward_kernel<false, 8>
+                                   : moe_combine_backward_kernel<false, 4>);
     return launch_pdl(kernel, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, st, 0, dy, lddy, ys, ldys, rows,
                       pos, weights, T, k, nvec, W, d_ys, ldd, d_w, status);
 }
