@@ -80,6 +80,46 @@ def test_pack_halves(sdt, size):
     check_pack(w, 32, sdt)
 
 
+@pytest.mark.parametrize("sdt", [bwt.F32, bwt.BF16])
+@pytest.mark.parametrize("exponent", [0, -50, 60])
+def test_pack_every_bf16_weight_below_a_maximum(sdt, exponent):
+    """Every 8-bit significand as the group's maximum, with every bf16 weight
+    from a 32nd of it upwards, both signs: among them all that lie exactly on a
+    half of the quotient or of the scale."""
+    rows = []
+    for b in range(128, 256):
+        v = np.array([a * 2.0 ** p for p in range(-5, 1) for a in range(128, 256)])
+        v = v[v <= b]
+        v = np.concatenate([v, np.zeros(-len(v) % 31)]).reshape(-1, 31)
+        v[:, ::2] *= -1
+        rows.append(np.concatenate([np.full((len(v), 1), float(b)), v], 1))
+        rows.append(-rows[-1])
+    check_pack((np.concatenate(rows) * 2.0 ** exponent).astype(np.float32), 32, sdt, bwt.BF16)
+
+
+@pytest.mark.parametrize("odt", [bwt.F32, bwt.BF16])
+@pytest.mark.parametrize("N,K,skip", [(1200, 9001, 0), (1200, 9002, 1), (40000, 250, 3), (2000, 5000, 1), (300, 31, 1)])
+def test_large_ragged_rows(odt, N, K, skip):
+    """Rows and bases without the alignment of wide accesses, at sizes where a
+    thread decodes several words; what lies beside the rows is left alone."""
+    group = 64
+    w = torch.randn(N, K, device="cuda").to(DT[odt])
+    wide = torch.full((N, K + 5), 3.0, dtype=DT[odt], device="cuda")
+    inside = wide.flatten()[skip:skip + (N - 1) * (K + 5) + K].as_strided((N, K), (K + 5, 1))
+    inside.copy_(w)
+    packed, s = bwt.lowbit_gs_pack(inside, group)
+    p2, s2 = bwt.lowbit_gs_pack(torch.nn.functional.pad(w, (0, -K % 8)), group)
+    assert torch.equal(s, s2[:, :s.shape[1]]) and torch.equal(packed, p2[:, :packed.shape[1]])
+    inside.fill_(7.0)
+    bwt.lowbit_gs_unpack(packed, s, K, group, odt, w=inside)
+    bits = torch.stack([(packed >> sh) & 15 for sh in (0, 4)], -1).view(N, -1, 4, 2).transpose(2, 3).reshape(N, -1)[:, :K]
+    codes = (bits ^ 8).float() - 8  # word by word: four low nibbles, then the high ones
+    want = (codes * s.repeat_interleave(group, 1)[:, :K]).to(DT[odt])
+    assert torch.equal(inside, want)
+    inside.fill_(3.0)
+    assert (wide == 3.0).all()
+
+
 def test_pack_zero_groups_and_signed_zero():
     w = weights(3, 4, 512)
     w[0] = 0.0
@@ -207,6 +247,22 @@ def test_linear_rows_past_32_bits(M):
     y = flat.as_strided((M, N), (ldy, 1))
     bwt.lowbit_gs_linear(q, s_x, packed, s_g, 64, y=y)
     assert torch.equal(y, want)
+
+
+def test_unpack_words_past_32_bits():
+    """More than 2^31 packed words (of 40 GB of values)."""
+    N, K = 600_000, 32768
+    if torch.cuda.mem_get_info()[0] < 70e9:
+        pytest.skip("needs 70 GB")
+    packed = torch.full((N, K // 2), 0x17, device="cuda", dtype=torch.uint8)  # codes 7 and 1
+    packed[-1], packed[N // 2] = 0x2E, 0xF3
+    s = torch.ones(N, K // 256, device="cuda", dtype=torch.bfloat16)
+    v = bwt.lowbit_gs_unpack(packed, s, K, 256, bwt.BF16)
+    low = [7.0] * 4 + [1.0] * 4
+    for r, word in ((0, low), (N - 2, low), (N - 1, [-2.0] * 4 + [2.0] * 4), (N // 2, [3.0] * 4 + [-1.0] * 4)):
+        assert torch.equal(v[r], torch.tensor(word * (K // 8), device="cuda", dtype=torch.bfloat16))
+    del v
+    torch.cuda.empty_cache()
 
 
 def test_unpack_values_past_32_bits():

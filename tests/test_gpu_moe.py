@@ -53,7 +53,8 @@ def test_plan_all_dropped_and_bad_ids(T):
 
 
 @pytest.mark.parametrize("dtype", [torch.int8, torch.bfloat16, torch.float32, torch.float64])
-@pytest.mark.parametrize("width,ld", [(1, 1), (3, 5), (64, 64), (100, 102), (1280, 1280), (1001, 1001), (5000, 5008)])
+@pytest.mark.parametrize("width,ld", [(1, 1), (3, 5), (64, 64), (100, 102), (1280, 1280), (1001, 1001), (5000, 5008),
+                                      (1004, 1004), (1002, 1002), (4098, 4098)])
 def test_gather(dtype, width, ld):
     T, k, E = 37, 3, 5
     off, pos = (cuda(a) for a in ref.plan(route(width, T, k, E, 0.3), E))
@@ -94,7 +95,9 @@ def combine_ref(ys, pos, w):
 
 @pytest.mark.parametrize("dt", [bwt.F32, bwt.BF16])
 @pytest.mark.parametrize("T,k,K,ld", [(1, 1, 1, 1), (3, 2, 7, 9), (40, 5, 64, 64), (16, 2, 1280, 1280),
-                                      (9, 8, 2560, 2560), (300, 4, 1001, 1003), (700, 9, 520, 520), (2, 3, 9000, 9000)])
+                                      (9, 8, 2560, 2560), (300, 4, 1001, 1003), (700, 9, 520, 520), (2, 3, 9000, 9000),
+                                      (60, 5, 1002, 1002), (90, 3, 1004, 1004), (7, 2, 4098, 4098),
+                                      (2500, 2, 1001, 1001)])
 def test_combine_and_gradients(dt, T, k, K, ld):
     E = 6
     rng = np.random.default_rng(T + K)
