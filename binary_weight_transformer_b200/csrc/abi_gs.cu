@@ -61,7 +61,7 @@ lowbit_status check_slots(const void *pos, int64_t T, int k, int64_t rows)
 // The kernel for a call, by its estimated time in ns, measured on a B200 (26 to
 // 9728 features, 1 to 4096 tokens, up to 128 experts).  The warp-level kernel
 // takes about 4.5 us, 0.5 us per 1000 codes of K and, per million weights (rows
-// in steps of 32) and pass of 16 tokens, 0.21 us (groups of 128 and 256) or 0.33
+// in steps of 16) and pass of 16 tokens, 0.21 us (groups of 128 and 256) or 0.33
 // us; gs_gemm_plan has the tcgen05 kernel's.  (Groups of 128, 64 tokens: 1280 ->
 // 3584 takes 8.6 us on either, 2560 -> 9728 27.5 and 14.9 us, 4096 -> 512 7.3 and
 // 10.9 us.)  Experts are taken to share the rows evenly, with half a pass more
@@ -76,7 +76,7 @@ lowbit_status gs_product(const GsArgs &a, cudaStream_t st)
     if (a.M <= 16 * active) return gs_mma_launch(a, st);
     const double rows = static_cast<double>(a.M) / static_cast<double>(active);
     const double passes = a.offsets == nullptr ? static_cast<double>((a.M + 15) / 16) : 1.3 * (rows / 16.0 + 0.5);
-    const double pass = (a.gshift >= 7 ? 210.0 : 330.0) * 1e-6 * static_cast<double>((a.N + 31) / 32 * 32) *
+    const double pass = (a.gshift >= 7 ? 210.0 : 330.0) * 1e-6 * static_cast<double>((a.N + 15) / 16 * 16) *
                         static_cast<double>(a.K);
     double mma = 4500.0 + 0.5 * static_cast<double>(a.K) + pass * passes * static_cast<double>(active);
     if (a.offsets != nullptr) {
@@ -105,6 +105,7 @@ lowbit_status lowbit_gs_pack(const void *w, lowbit_dtype wdt, int64_t N, int64_t
     const lowbit_status a = check_artifact(packed, ldp, s_g, sdt, lds, N, K, group);
     if (a != LOWBIT_OK) return a;
     if (ldw < K) return LOWBIT_ERR_INVALID_ARG;
+    if (ldp >= int64_t(1) << 30) return LOWBIT_ERR_UNSUPPORTED;
     if (!aligned(w, size_of(wdt))) return LOWBIT_ERR_ALIGNMENT;
     const lowbit_status d = check_device();
     if (d != LOWBIT_OK) return d;

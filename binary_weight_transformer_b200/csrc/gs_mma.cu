@@ -28,6 +28,12 @@
 // weights) and the scales.  The warps of a block, and the blocks of a cluster,
 // that share rows add their fp32 tiles in a fixed order, the latter through
 // distributed shared memory.
+//
+// Measured on a B200, groups of 128: 9728 -> 2560 with 16 tokens 10.2 us (12.8 MB
+// of weights and scales: 19% of the copy bandwidth; latency: the launch, one
+// round trip for codes and weights, eight units of arithmetic per warp, two
+// cluster barriers), 2560 -> 9728 10.3; eight experts of 1280 -> 3584 with 32
+// rows 10.5 us.  A second wave of blocks costs 3 us.
 #include "gs_internal.cuh"
 #include "tc_common.cuh"
 

@@ -11,9 +11,16 @@
 // shuffles.  32 (fp32) or 16 (bf16) bytes per lane in flight at full occupancy
 // cover the memory latency; what held the packer back was instructions (25 per
 // weight at first: 64-bit divisions for the address, an IEEE division and
-// reciprocal per lane).  A lane's eight fp32 values are
-// one 32-byte access where rows allow it: as two of 16 bytes, every 32-byte
-// sector crosses the L2 twice.
+// reciprocal per lane), which still keep the issue slots 70 to 80% busy.
+// A lane's eight fp32 values are one 32-byte access where rows allow it: as two
+// of 16 bytes, every 32-byte sector crosses the L2 twice.  Other rows are read
+// and written 32 values at a time, through shared memory.
+//
+// Measured on a B200, groups of 128: 9728 x 2560 fp32 packs in 20.9 us (5.4
+// TB/s, 82% of the copy bandwidth) and unpacks in 19.1 (5.9 TB/s); 5815 x 9000
+// bf16 in 37.9 and 25.7 us (3.5 and 5.1 TB/s), 5815 x 9001 bf16 in 49 and 41.
+// Two or four pieces per warp, with their loads in flight together, were slower
+// (21.8 to 28 us): fewer warps fit.
 #include "gs_internal.cuh"
 
 namespace lowbit {
@@ -457,7 +464,7 @@ lowbit_status gs_pack_launch(const void *w, int w_bf16, int64_t N, int64_t K, in
 {
     const int64_t units = (ldp * 2 + kUnit - 1) / kUnit;
     const int64_t blocks = (N + kThreads / 32 - 1) / (kThreads / 32) * units;
-    if (blocks > INT32_MAX || units > INT32_MAX / kUnit) return LOWBIT_ERR_UNSUPPORTED;
+    if (blocks > INT32_MAX) return LOWBIT_ERR_UNSUPPORTED;
     const PackArgs a = {w, N, K, ldw, rows_aligned(w, ldw, w_bf16 ? 2 : 4) ? 1 : 0, static_cast<uint32_t>(units), packed, ldp,
                         static_cast<uint8_t *>(s_g), lds, status, static_cast<unsigned>(blocks), st};
     return w_bf16 ? (s_bf16 ? pack_groups<true, true>(a, gshift) : pack_groups<true, false>(a, gshift))

@@ -10,6 +10,13 @@
 // combine and backward run by token, which reads a token's row (x, dy) once
 // for its k slots instead of once per slot, and needs only pos.  No atomics
 // on data: every output value has one writer and a fixed order of additions.
+//
+// Measured on a B200, 8192 tokens of 2560 bf16 features, four slots each, 64
+// experts, 5% dropped: plan 8.8 us (latency: two passes over 128 slots per warp
+// and a scan over warps, blocks and experts), gather 32.9 (201 MB, 6.1 TB/s), combine
+// 35.4 (5.7 TB/s), backward 59 (360 MB, 6.1 TB/s).  Rows of other alignments
+// take narrower accesses: 4096 tokens of 1001, 1002 and 1004 bf16 features,
+// combined with gradients, take 49, 29 and 24 us.
 #include <type_traits>
 
 #include "gs_internal.cuh"

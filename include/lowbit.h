@@ -487,8 +487,9 @@ int64_t lowbit_gs_groups(int64_t K, int group);
  *              gives zero codes.
  * Outputs: packed [N, ldp] (ldp >= lowbit_packed_row_bytes(LOWBIT_INT4, K), a
  * multiple of 16, 16-byte aligned base; unowned bits of all ldp bytes written
- * zero), s_g [N, lds], lds >= lowbit_gs_groups(K, group).  w is aligned to its
- * element size (rows on 16-byte boundaries take vector loads).  A non-finite
+ * zero; ldp < 2^30), s_g [N, lds], lds >= lowbit_gs_groups(K, group).  w is
+ * aligned to its element size (rows on boundaries of eight elements are
+ * fastest).  A non-finite
  * weight sets LOWBIT_ERR_NONFINITE in *status_dev; its group is then
  * unspecified. */
 lowbit_status lowbit_gs_pack(const void *w, lowbit_dtype wdt, int64_t N, int64_t K, int64_t ldw, int group,
@@ -508,7 +509,10 @@ lowbit_status lowbit_gs_unpack(const uint8_t *packed, int64_t ldp, const void *s
  * acc_g is exact; the sum over groups is fp32 in an order fixed by the sizes
  * (the same call gives the same bits); y is fp32 or bf16 (LOWBIT_I32 is not
  * possible here).  q, s_x, y and their alignments as lowbit_linear; flags: 0
- * or LOWBIT_LINEAR_WEIGHTS_STABLE (packed and s_g). */
+ * or LOWBIT_LINEAR_WEIGHTS_STABLE (packed and s_g; the kernels for few tokens
+ * then load them before the previous kernel ends).  One token runs on dp4a,
+ * few on warp-level MMA, many on tcgen05; from 17 on the one with the smaller
+ * estimated time. */
 lowbit_status lowbit_gs_linear(const int8_t *q, int64_t ldq, const float *s_x, int64_t M, int64_t K,
                                const uint8_t *packed, int64_t ldp, const void *s_g, lowbit_dtype sdt, int64_t lds,
                                int group, int64_t N, void *y, lowbit_dtype ydt, int64_t ldy, unsigned flags,
@@ -522,7 +526,9 @@ lowbit_status lowbit_gs_linear(const int8_t *q, int64_t ldq, const float *s_x, i
  * scales, or rows of any other type) into that order;
  * lowbit_gs_linear_experts applies each expert's weights to its rows;
  * lowbit_moe_combine adds the k rows of a token with its routing weights.
- * Nothing here synchronises the host: row counts stay on the device.
+ * Nothing here synchronises the host: row counts stay on the device.  Where
+ * pos is read, each row is named at most once, as lowbit_moe_plan's are: the
+ * content of a row that is named twice is one of the two.
  * ------------------------------------------------------------------------- */
 #define LOWBIT_MOE_MAX_EXPERTS 1024
 

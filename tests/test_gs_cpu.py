@@ -40,6 +40,11 @@ def test_pack_and_unpack_refuse(lib, change, want):
                                 a["wdt"], a["ldw"], None, None) == want
 
 
+def test_pack_refuses_rows_of_a_gigabyte(lib):
+    """The packer writes all of a row's ldp bytes and addresses them in 31 bits."""
+    assert lib.lowbit_gs_pack(FAKE, bwt.F32, 8, 256, 256, 128, FAKE, 2 ** 30, FAKE, bwt.F32, 2, None, None) == UNSUPPORTED
+
+
 TOKENS = dict(q=FAKE, ldq=256, s_x=FAKE, M=4, N=8, K=256, y=FAKE, ydt=bwt.F32, ldy=8)
 BAD_TOKENS = [
     (dict(q=None), INVALID), (dict(s_x=None), INVALID), (dict(y=None), INVALID), (dict(M=0), INVALID),
