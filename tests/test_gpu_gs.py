@@ -1,5 +1,9 @@
 """Group-scaled 4-bit weights on the GPU: packer, values, and the linear layer
 against their 64-bit definitions."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -247,6 +251,62 @@ def test_linear_rows_past_32_bits(M):
     y = flat.as_strided((M, N), (ldy, 1))
     bwt.lowbit_gs_linear(q, s_x, packed, s_g, 64, y=y)
     assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("M", [1, 5, 40, 200])
+def test_linear_operands_past_32_bits(M):
+    """Rows of codes, packed weights and scales whose byte offsets pass 2^31."""
+    N, K, group = 40, 1280, 64
+    packed, s_g = bwt.lowbit_gs_pack(cuda(weights(5, N, K)), group)
+    q, s_x = (cuda(a) for a in tokens(6, M, K))
+    want = bwt.lowbit_gs_linear(q, s_x, packed, s_g, group)
+
+    def apart(t, ld):
+        flat = torch.empty((len(t) - 1) * ld + t.shape[1], dtype=t.dtype, device="cuda")
+        far = flat.as_strided(t.shape, (ld, 1))
+        far.copy_(t)
+        return far
+
+    far = [apart(packed, 2 ** 26), apart(s_g, 2 ** 25 + 1)]
+    q = apart(q, (2 ** 31 // (M - 1) + 16) // 16 * 16) if M > 1 else q
+    assert torch.equal(bwt.lowbit_gs_linear(q, s_x, *far, group, K=K), want)
+
+
+def test_first_calls_inside_a_capture():
+    """In a fresh process: what a kernel sets up on its first call may happen
+    while a graph is captured."""
+    code = """
+import torch, binary_weight_transformer_b200 as bwt
+torch.cuda.init()
+w = torch.randn(600, 1280, device="cuda")
+x = torch.randn(500, 1280, device="cuda")
+e = torch.randint(0, 4, (500, 2), device="cuda", dtype=torch.int32)
+r = torch.rand(500, 2, device="cuda")
+bwt.lib()
+
+def run():
+    p, s = bwt.lowbit_gs_pack(w, 64)
+    v = bwt.lowbit_gs_unpack(p, s, 1280, 64)
+    q, sx = bwt.lowbit_act_quant(x)
+    ys = [bwt.lowbit_gs_linear(q[:m], sx[:m], p, s, 64) for m in (1, 9, 500)]
+    off, pos = bwt.lowbit_moe_plan(e, 4)
+    qs, ss = bwt.lowbit_moe_gather(q, pos, s_x=sx)
+    z = bwt.lowbit_gs_linear_experts(qs, ss, off, p.view(4, 150, -1), s.view(4, 150, -1), 64)
+    y = bwt.lowbit_moe_combine(z, pos, r)
+    return [v, *ys, y, *bwt.lowbit_moe_combine_backward(y, z, pos, r)]
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    out = run()
+g.replay()
+want = run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, want))
+print("same")
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    run = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.strip() == "same", run.stderr[-2000:]
 
 
 def test_unpack_words_past_32_bits():

@@ -239,6 +239,52 @@ def test_experts_strides(counts):
     check_experts(counts, 500, 72, 128, bwt.F32, bwt.BF16, strided=True, spare=200)
 
 
+@pytest.mark.parametrize("counts", [[3, 0, 5], [150, 40, 200]])
+def test_experts_apart_past_32_bits(counts):
+    """Experts whose weights and scales lie more than 2^31 bytes apart."""
+    K, N, group = 640, 40, 64
+    _, _, packed, s_g = expert_weights(4, 3, N, K, group, bwt.F32)
+    q = torch.randint(-128, 128, (sum(counts), K), dtype=torch.int8, device="cuda")
+    s_x = torch.rand(sum(counts), device="cuda")
+    off = cuda(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32))
+    want = bwt.lowbit_gs_linear_experts(q, s_x, off, packed, s_g, group)
+
+    def apart(t, step):
+        far = torch.empty(2 * step + t[0].numel(), dtype=t.dtype, device="cuda").as_strided(t.shape, (step, *t.stride()[1:]))
+        far.copy_(t)
+        return far
+
+    got = bwt.lowbit_gs_linear_experts(q, s_x, off, apart(packed, 2 ** 31 + 64), apart(s_g, 2 ** 30 + 3), group)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dt", [bwt.F32, bwt.BF16])
+def test_routing_rows_past_32_bits(dt):
+    """Rows of gather, combine and its gradient more than 2^31 elements in."""
+    T, k, K, E = 6, 2, 1001, 3
+    _, pos = ref.plan(route(8, T, k, E), E)
+    tp, w = cuda(pos), torch.rand(T, k, device="cuda")
+    x, dy = (torch.randn(T, K, device="cuda").to(DT[dt]) for _ in range(2))
+
+    def apart(rows):
+        ld = 2 ** 31 // (rows - 1) + 5
+        return torch.zeros((rows - 1) * ld + K, dtype=DT[dt], device="cuda").as_strided((rows, K), (ld, 1))
+
+    ys = bwt.lowbit_moe_gather(x, tp)
+    far_ys = apart(T * k)
+    bwt.lowbit_moe_gather(x, tp, out=far_ys)
+    assert torch.equal(far_ys, ys)
+    y, far_y = bwt.lowbit_moe_combine(ys, tp, w), apart(T)
+    bwt.lowbit_moe_combine(far_ys, tp, w, y=far_y)
+    assert torch.equal(far_y, y)
+    d_ys, d_w = bwt.lowbit_moe_combine_backward(dy, ys, tp, w)
+    far_y.copy_(dy)
+    far_d, far_w = bwt.lowbit_moe_combine_backward(far_y, far_ys, tp, w, d_ys=apart(T * k))
+    assert torch.equal(far_d, d_ys)
+    size = (ys.float().abs().max() * dy.float().abs().max()).item() * K
+    assert (far_w - d_w).abs().max().item() <= 2 * (K + 2) * ref.U32 * size  # two orders of one sum
+
+
 @pytest.mark.parametrize("rows", [16, 400])
 def test_experts_without_tokens(rows):
     y = torch.full((rows, 32), 4.0, device="cuda")

@@ -1,5 +1,8 @@
 """Refusals of the group-scaled and routing calls, and the definitions the GPU
 tests compare against; no GPU is used and no call here reaches a launch."""
+import os
+import re
+
 import numpy as np
 import pytest
 import torch
@@ -181,3 +184,23 @@ def test_reference_plan_on_a_worked_table():
     off, pos = ref.plan(np.array([[2, 0], [-1, 2], [0, 2]]), 3)
     assert off.tolist() == [0, 2, 2, 5]
     assert pos.tolist() == [[2, 0], [-1, 3], [1, 4]]
+
+
+def test_registers():
+    """The tcgen05 kernel splits its registers after launch (256 threads of 64,
+    256 of 192), which needs the 128 per thread that it is compiled for; the
+    packer runs at 2048 threads per SM."""
+    from binary_weight_transformer_b200 import _build
+    _build.build()
+    seen = {"gs_gemm": 0, "gs_pack": 0}
+    for name, regs, spill in (("gs_gemm", 128, 16), ("gs_pack", 32, 8)):
+        path = os.path.join(os.path.dirname(_build.__file__), "_build", name + ".cu.ptxas.txt")
+        if not os.path.exists(path):
+            pytest.skip("no ptxas report (library built elsewhere)")
+        for m in re.finditer(r"Compiling entry function '([^']+)'.*?(\d+) bytes spill stores.*?Used (\d+) registers",
+                             open(path).read(), re.S):
+            if name + "_kernel" in m.group(1):
+                seen[name] += 1
+                assert int(m.group(2)) <= spill, m.group(1)
+                assert int(m.group(3)) == regs if name == "gs_gemm" else int(m.group(3)) <= regs, m.group(1)
+    assert seen == {"gs_gemm": 16, "gs_pack": 32}
