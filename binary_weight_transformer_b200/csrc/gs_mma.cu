@@ -32,7 +32,7 @@
 // Measured on a B200, groups of 128: 9728 -> 2560 with 16 tokens 10.2 us (12.8 MB
 // of weights and scales: 19% of the copy bandwidth; latency: the launch, one
 // round trip for codes and weights, eight units of arithmetic per warp, two
-// cluster barriers), 2560 -> 9728 10.3; eight experts of 1280 -> 3584 with 32
+// cluster barriers), 2560 -> 9728 10.9; eight experts of 1280 -> 3584 with 32
 // rows 10.5 us.  A second wave of blocks costs 3 us.
 #include "gs_internal.cuh"
 #include "tc_common.cuh"
@@ -41,8 +41,7 @@ namespace lowbit {
 namespace gsm {
 
 constexpr int kUnit = 128;     // codes of a row per warp step
-constexpr int kRowWarps = 4;   // warps of a block along the weight rows
-constexpr int kMaxKWarps = 2;  // and along K
+constexpr int kWarps = 8;      // most warps of a block: RW along the weight rows, kWarps / RW along K
 constexpr int kMaxSplit = 8;   // blocks of a cluster, along K
 constexpr int kAhead = 8;      // units of a warp in flight
 
@@ -145,8 +144,8 @@ struct Split {
 
 // TOK: tokens per pass, 8 or 16.  (Passes of 32 tokens, with 16 rows per warp,
 // took 24 us for 2560 -> 9728 at M = 32, two passes of 16 take 16 us.)
-template <int TOK, int GM>
-__global__ void __launch_bounds__(kRowWarps * kMaxKWarps * 32, TOK == 16 ? 3 : 4)
+template <int TOK, int GM, int RW>
+__global__ void __launch_bounds__(kWarps * 32, TOK == 16 ? 3 : 4)
 gs_mma_kernel(const GsArgs a, const Split sp)
 {
     constexpr int EL = TOK == 8 ? 2 : 4;         // C elements in use: sums per lane
@@ -154,11 +153,13 @@ gs_mma_kernel(const GsArgs a, const Split sp)
     constexpr int kGroups = GM == kG32 ? 4 : GM == kG64 ? 2 : 1;  // groups of a unit
     constexpr int kSteps = 4 / kGroups;
     constexpr int kPair = 2;                     // units multiplied together
-    constexpr int kRows = 8 * kRowWarps;         // weight rows of a block
+    constexpr int kRows = 8 * RW;                // weight rows of a block
+    constexpr int kMaxKWarps = kWarps / RW;
+    static_assert(kRows / kWarps % 4 == 0, "a warp stages the scales of four rows at a time");
     extern __shared__ __align__(16) uint8_t smem[];  // codes, scales, rings; then the sums that are added
     __shared__ float sx[TOK];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    const int rw = warp & (kRowWarps - 1), kw = warp / kRowWarps;
+    const int rw = warp & (RW - 1), kw = warp / RW;
     const int g = lane >> 2, t = lane & 3;
     const int n_block = static_cast<int>(blockIdx.x) * kRows;
     const int n0 = n_block + rw * 8;
@@ -204,7 +205,7 @@ gs_mma_kernel(const GsArgs a, const Split sp)
 
         for (int c0 = u_lo; c0 < u_hi; c0 += sp.chunk) {
             const int c1 = c0 + sp.chunk < u_hi ? c0 + sp.chunk : u_hi;
-            const int share = ((c1 - c0) / kRun * kRowWarps + warps - 1) / warps * kRun;  // units per K warp
+            const int share = ((c1 - c0) / kRun * RW + warps - 1) / warps * kRun;  // units per K warp
             const int v0 = c0 + kw * share;
             const int v1 = v0 + share < c1 ? v0 + share : c1;
             // this lane's units to fetch: [v0, end); zeros from there on
@@ -249,7 +250,7 @@ gs_mma_kernel(const GsArgs a, const Split sp)
             const int g_lo = c0 * kGroups / kRun, g_n = (c1 - c0) * kGroups / kRun;
             const int g_all = static_cast<int>((a.K - 1) >> a.gshift) + 1;
             for (int i = lane; i < g_n; i += 32) {
-                constexpr int kMost = kRows / kRowWarps;  // rows of a warp
+                constexpr int kMost = 8;  // most rows of a warp
                 const int rows = kRows / warps, rr0 = warp * rows;
                 const bool in_row = g_lo + i < g_all;
                 const int64_t at = (n_block + rr0) * a.lds + g_lo + i;
@@ -337,15 +338,15 @@ gs_mma_kernel(const GsArgs a, const Split sp)
                 else static_cast<float *>(a.y)[(tok + tk) * a.ldy + n] = f;
             }
         };
-        if (sp.split == 1 && warps == kRowWarps) {
+        if (sp.split == 1 && warps == RW) {
 #pragma unroll
             for (int e = 0; e < EL; ++e) put(e, lane, n0, acc[e]);
         } else {
             __syncthreads();  // the staged codes are read
             float *sums = reinterpret_cast<float *>(smem);  // [K warp][element][row warp, lane]
-            constexpr int kTile = EL * kRowWarps * 32;
+            constexpr int kTile = EL * RW * 32;
 #pragma unroll
-            for (int e = 0; e < EL; ++e) sums[kw * kTile + e * (kRowWarps * 32) + rw * 32 + lane] = acc[e];
+            for (int e = 0; e < EL; ++e) sums[kw * kTile + e * (RW * 32) + rw * 32 + lane] = acc[e];
             if (sp.split > 1) tc::cluster_sync_all();
             else __syncthreads();
             // each block adds its share of the tile: K warps within ranks, ranks in order
@@ -356,7 +357,7 @@ gs_mma_kernel(const GsArgs a, const Split sp)
 #pragma unroll
                     for (int k = 0; k < kMaxKWarps; ++k) {
                         part[p][k] = 0.0f;
-                        if (p < sp.split && k * kRowWarps < warps) {
+                        if (p < sp.split && k * RW < warps) {
                             const uint32_t at = q_base + static_cast<uint32_t>((k * kTile + i) * 4);
                             asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part[p][k])
                                          : "r"(sp.split > 1 ? tc::map_to_peer(at, static_cast<uint32_t>(p)) : at) : "memory");
@@ -367,8 +368,8 @@ gs_mma_kernel(const GsArgs a, const Split sp)
                 for (int p = 0; p < kMaxSplit; ++p)
 #pragma unroll
                     for (int k = 0; k < kMaxKWarps; ++k) v += part[p][k];
-                const int th = i % (kRowWarps * 32);
-                put(i / (kRowWarps * 32), th & 31, n_block + (th >> 5) * 8, v);
+                const int th = i % (RW * 32);
+                put(i / (RW * 32), th & 31, n_block + (th >> 5) * 8, v);
             }
             if (sp.split > 1) tc::cluster_sync_all();  // peers have read this block's sums
         }
@@ -400,10 +401,11 @@ lowbit_status launch_clusters_y(void (*kernel)(KArgs...), dim3 grid, dim3 block,
     return launch_status();
 }
 
-template <int TOK, int GM>
+template <int TOK, int GM, int RW>
 lowbit_status launch(const GsArgs &a, cudaStream_t st)
 {
-    constexpr int kRows = 8 * kRowWarps;
+    constexpr int kRows = 8 * RW;
+    constexpr int kMaxKWarps = kWarps / RW;
     constexpr int kElems = TOK == 8 ? 2 : 4;
     constexpr int kRun = GM == kG256 ? 2 : 1;
     constexpr int kGroups = GM == kG32 ? 4 : GM == kG64 ? 2 : 1;
@@ -422,11 +424,17 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
     }
     // Ranges of K per row block: as many as make a warp's range about four
     // units, as long as all warps are resident at once.
-    const int64_t fit = static_cast<int64_t>(device_sm_count()) * (TOK == 8 ? 32 : 24) / (slabs * active * kRowWarps);
+    const int64_t fit = static_cast<int64_t>(device_sm_count()) * (TOK == 8 ? 32 : 24) / (slabs * active * RW);
     int64_t ranges = (units + 3) / 4;
     if (ranges > fit) ranges = fit;
     if (ranges > runs) ranges = runs;
-    const int64_t kwarps = ranges < 2 ? 1 : kMaxKWarps;
+    // Two or three ranges: two warps of a block, without a cluster (12 tokens,
+    // 1280 -> 3584: 5.0 us against 6.2 for a cluster of three).  Six to eight: two
+    // in each block of a cluster of three or four (16 tokens, 4096 -> 512: 5.2
+    // against 5.4 for eight blocks).  Else blocks only, in larger clusters but
+    // with shorter ranges (4 tokens, 9728 -> 2560: 10.1 against 11.3; 8 tokens,
+    // 2560 -> 2560: 6.3 against 6.9).
+    const int64_t kwarps = kMaxKWarps > 1 && ranges >= 2 && (ranges <= 3 || (ranges >= 6 && ranges <= 8)) ? kMaxKWarps : 1;
     int64_t split = ranges / kwarps;
     if (split < 1) split = 1;
     if (split > kMaxSplit) split = kMaxSplit;
@@ -436,35 +444,46 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
     const int64_t chunk = per * kRun < max_chunk<TOK>() ? per * kRun : max_chunk<TOK>();
     const auto bytes = [](int64_t units_, int64_t kwarps_) {
         return static_cast<size_t>(TOK) * q_stride<GM>(static_cast<int>(units_)) +
-               static_cast<size_t>(kRows * units_ * kGroups / kRun * 4) + kRowWarps * kwarps_ * kAhead * 512;
+               static_cast<size_t>(kRows * units_ * kGroups / kRun * 4) + RW * kwarps_ * kAhead * 512;
     };
     size_t smem = bytes(chunk, kwarps);
-    const size_t sums = static_cast<size_t>(kElems) * kRowWarps * kwarps * 32 * 4;
+    const size_t sums = static_cast<size_t>(kElems) * RW * kwarps * 32 * 4;
     if (smem < sums) smem = sums;
     static PerDevice configured;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return LOWBIT_ERR_CUDA;
     if (configured.get(dev, [&] {
-            return cudaFuncSetAttribute(gs_mma_kernel<TOK, GM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            return cudaFuncSetAttribute(gs_mma_kernel<TOK, GM, RW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                         static_cast<int>(bytes(max_chunk<TOK>(), kMaxKWarps))) == cudaSuccess ? 1 : 0;
         }) <= 0)
         return LOWBIT_ERR_CUDA;
     const Split sp = {static_cast<int>(units), static_cast<int>(per), static_cast<int>(chunk), static_cast<int>(split),
                       static_cast<int>(lanes)};
-    return launch_clusters_y(gs_mma_kernel<TOK, GM>,
+    return launch_clusters_y(gs_mma_kernel<TOK, GM, RW>,
                              dim3(static_cast<unsigned>(slabs), static_cast<unsigned>(split), static_cast<unsigned>(ztiles)),
-                             dim3(static_cast<unsigned>(kRowWarps * kwarps * 32)), smem, st, static_cast<unsigned>(split), a,
+                             dim3(static_cast<unsigned>(RW * kwarps * 32)), smem, st, static_cast<unsigned>(split), a,
                              sp);
+}
+
+template <int TOK, int GM>
+lowbit_status launch_r(const GsArgs &a, cudaStream_t st)
+{
+    // Blocks of 64 rows where 32 would be two or more per SM: they stage a
+    // token's codes half as often (16 tokens, 2560 -> 9728: 10.9 against 12.4
+    // us).  Not for experts, whose blocks are uneven (64 experts of 2048 -> 768
+    // with 32 rows: 12.0 against 10.4).
+    const bool tall = a.offsets == nullptr && (a.N + 31) / 32 * ((a.M + TOK - 1) / TOK) >= 2 * device_sm_count();
+    return tall ? launch<TOK, GM, 8>(a, st) : launch<TOK, GM, 4>(a, st);
 }
 
 template <int TOK>
 lowbit_status launch_g(const GsArgs &a, cudaStream_t st)
 {
     switch (a.gshift) {
-    case 5: return launch<TOK, kG32>(a, st);
-    case 6: return launch<TOK, kG64>(a, st);
-    case 7: return launch<TOK, kG128>(a, st);
-    default: return launch<TOK, kG256>(a, st);
+    case 5: return launch_r<TOK, kG32>(a, st);
+    case 6: return launch_r<TOK, kG64>(a, st);
+    case 7: return launch_r<TOK, kG128>(a, st);
+    default: return launch_r<TOK, kG256>(a, st);
     }
 }
 
@@ -474,7 +493,7 @@ int64_t gs_mma_lanes(const GsArgs &a, int tok)
 {
     const int64_t active = a.E < a.M ? a.E : a.M, passes = (a.M + active * tok - 1) / (active * tok);
     if (passes < 2) return 1;
-    const int64_t slabs = (a.N + 8 * gsm::kRowWarps - 1) / (8 * gsm::kRowWarps);
+    const int64_t slabs = (a.N + 31) / 32;
     int64_t lanes = device_sm_count() * 3 / (slabs * active);
     if (lanes > 2 * passes) lanes = 2 * passes;
     if (lanes * a.E > 65535) lanes = 65535 / a.E;
