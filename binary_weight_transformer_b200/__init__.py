@@ -446,15 +446,16 @@ def lowbit_rescale(acc, s_x, s_w, fmt: int, out_dtype: int = F32, y=None, status
 # These calls take a few microseconds on the device for small inputs, so the
 # checks below are written for the host's time: one expression per tensor, no
 # strides asked of a contiguous one, the current stream's handle without a
-# Stream object (which takes 3 us), and the details of a refusal worked out
-# only when there is one.
+# Stream object (which takes 3 us), outputs made from a tensor at hand (0.5 to 1
+# us less than by type and device), and the details of a refusal worked out only
+# when there is one.
 # ---------------------------------------------------------------------------
 class _Torch:
     """torch and what the calls below need of it, looked up at the first call."""
 
     def __init__(self):
         import torch
-        self.torch, self.empty = torch, torch.empty
+        self.torch, self.empty_like = torch, torch.empty_like
         self.i8, self.u8, self.i32, self.i64, self.f32 = (torch.int8, torch.uint8, torch.int32, torch.int64,
                                                           torch.float32)
         self.kind = {torch.float32: F32, torch.bfloat16: BF16}  # lowbit_dtype of a real type
@@ -575,11 +576,11 @@ def lowbit_gs_pack(w, group: int = 128, scale_dtype: int = F32, packed=None, s_g
     dev, N, K, ldw = _matrix(w, "w", w.dtype)
     G = gs_groups(K, group)
     if packed is None:
-        packed = tt.empty((N, ldp if ldp is not None else (K + 31) // 32 * 16), dtype=tt.u8, device=dev)
+        packed = w.new_empty((N, ldp if ldp is not None else (K + 31) // 32 * 16), dtype=tt.u8)
     elif _matrix(packed, "packed", tt.u8)[:2] != (dev, N) or not packed.is_contiguous():
         raise ValueError(f"packed must be contiguous with {N} rows on cuda:{dev}")
     if s_g is None:
-        s_g = tt.empty((N, G), dtype=sdt, device=dev)
+        s_g = w.new_empty((N, G), dtype=sdt)
     lds = _rows(s_g, "s_g", N, G, sdt, dev)
     _call("lowbit_gs_pack", dev, status, stream, w.data_ptr(), kind, N, K, ldw, group, packed.data_ptr(),
           packed.shape[1], s_g.data_ptr(), scale_dtype, lds)
@@ -594,7 +595,7 @@ def lowbit_gs_unpack(packed, s_g, K: int, group: int = 128, out_dtype: int = F32
     _fits(width, K)
     lds = _rows(s_g, "s_g", N, gs_groups(K, group), s_g.dtype, dev)
     if w is None:
-        w = tt.empty((N, K), dtype=dt, device=dev)
+        w = packed.new_empty((N, K), dtype=dt)
     ldw = _rows(w, "w", N, K, dt, dev)
     _call("lowbit_gs_unpack", dev, status, stream, packed.data_ptr(), ldp, s_g.data_ptr(), kind, lds, N, K, group,
           w.data_ptr(), out_dtype, ldw)
@@ -624,7 +625,7 @@ def lowbit_gs_linear(q, s_x, packed, s_g, group: int = 128, out_dtype: int = F32
     _fits(width, K)
     lds = _rows(s_g, "s_g", N, gs_groups(K, group), s_g.dtype, dev)
     if y is None:
-        y = tt.empty((M, N), dtype=dt, device=dev)
+        y = q.new_empty((M, N), dtype=dt)
         ldy = N
     else:
         ldy = _rows(y, "y", M, N, dt, dev)
@@ -667,7 +668,7 @@ def lowbit_gs_linear_experts(q, s_x, offsets, packed, s_g, group: int = 128, out
         lds = _strides(s_g, "s_g")
         sstride = s_g.stride(0) if E > 1 else N * lds
     if y is None:
-        y = tt.empty((R, N), dtype=dt, device=dev)
+        y = q.new_empty((R, N), dtype=dt)
         ldy = N
     else:
         ldy = _rows(y, "y", R, N, dt, dev)
@@ -688,11 +689,11 @@ def lowbit_moe_plan(experts, E: int, offsets=None, pos=None, status=None, stream
     if not experts.is_contiguous():
         raise ValueError("experts must be contiguous")
     if offsets is None:
-        offsets = tt.empty(E + 1, dtype=tt.i32, device=dev)
+        offsets = experts.new_empty(E + 1, dtype=tt.i32)
     else:
         _vector(offsets, "offsets", E + 1, tt.i32, dev)
     if pos is None:
-        pos = tt.empty((T, k), dtype=tt.i32, device=dev)
+        pos = tt.empty_like(experts, dtype=tt.i32)
     else:
         _slots(pos, "pos", tt.i32, T, k, dev)
     _call("lowbit_moe_plan", dev, status, stream, experts.data_ptr(), 1 if dtype is tt.i64 else 0, T, k, E,
@@ -712,7 +713,7 @@ def lowbit_moe_gather(x, pos, s_x=None, out=None, s_out=None, status=None, strea
     _slots(pos, "pos", tt.i32, T, k, dev)
     if out is None:
         rows, ldo = T * k, width
-        out = tt.empty((rows, width), dtype=dtype, device=dev)
+        out = x.new_empty((rows, width))
     else:
         rows = out.shape[0]
         ldo = _rows(out, "out", rows, width, dtype, dev)
@@ -720,7 +721,7 @@ def lowbit_moe_gather(x, pos, s_x=None, out=None, s_out=None, status=None, strea
     if s_x is not None:
         _vector(s_x, "s_x", T, tt.f32, dev)
         if s_out is None:
-            s_out = tt.empty(rows, dtype=tt.f32, device=dev)
+            s_out = s_x.new_empty(rows)
         else:
             _vector(s_out, "s_out", rows, tt.f32, dev)
         from_s, to_s = s_x.data_ptr(), s_out.data_ptr()
@@ -747,7 +748,7 @@ def lowbit_moe_combine(ys, pos, weights=None, y=None, status=None, stream=None):
         _slots(weights, "weights", tt.f32, T, k, dev)
         w = weights.data_ptr()
     if y is None:
-        y = tt.empty((T, K), dtype=dtype, device=dev)
+        y = ys.new_empty((T, K))
         ldy = K
     else:
         ldy = _rows(y, "y", T, K, dtype, dev)
@@ -768,12 +769,12 @@ def lowbit_moe_combine_backward(dy, ys, pos, weights, d_ys=None, d_w=None, statu
     _slots(pos, "pos", tt.i32, T, k, dev)
     _slots(weights, "weights", tt.f32, T, k, dev)
     if d_ys is None:
-        d_ys = tt.empty((R, K), dtype=dtype, device=dev)
+        d_ys = ys.new_empty((R, K))
         ldd = K
     else:
         ldd = _rows(d_ys, "d_ys", R, K, dtype, dev)
     if d_w is None:
-        d_w = tt.empty((T, k), dtype=tt.f32, device=dev)
+        d_w = tt.empty_like(weights)
     else:
         _slots(d_w, "d_w", tt.f32, T, k, dev)
     _call("lowbit_moe_combine_backward", dev, status, stream, dy.data_ptr(), lddy, ys.data_ptr(), ldys, kind, R,
