@@ -36,7 +36,8 @@
 // takes four times its share: 728 us; with 256 the MMA thread bounds: 212 us.
 // Measured and slower: scalar multiply-adds (297 us), conversion by integer
 // addition and a subtraction for an eighth to three quarters of the sums (262 to
-// 279), accumulators that start at the conversion's bias, 128-token tiles.
+// 279), accumulators that start at the conversion's bias, 128-token tiles, 16
+// drain warps of 64 columns with loads of 8 (288).
 #include "gs_internal.cuh"
 #include "tc_common.cuh"
 
