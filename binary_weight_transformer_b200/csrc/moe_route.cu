@@ -12,9 +12,10 @@
 // on data: every output value has one writer and a fixed order of additions.
 //
 // Measured on a B200, 8192 tokens of 2560 bf16 features, four slots each, 64
-// experts, 5% dropped: plan 8.8 us (latency: two passes over 128 slots per warp
-// and a scan over warps, blocks and experts), gather 32.9 (201 MB, 6.1 TB/s), combine
-// 35.4 (5.7 TB/s), backward 59 (360 MB, 6.1 TB/s).  Rows of other alignments
+// experts, 5% dropped: plan 6.4 us (latency: matches within 128 slots per warp, 8.8
+// when the second pass repeated them, and a scan over warps, blocks and experts),
+// gather 33.2 (201 MB, 6.1 TB/s), combine 35.4 (5.7 TB/s), backward 60 (360 MB,
+// 6.0 TB/s).  Rows of other alignments
 // take narrower accesses: 4096 tokens of 1001, 1002 and 1004 bf16 features,
 // combined with gradients, take 49, 29 and 24 us.
 #include <type_traits>
@@ -47,8 +48,9 @@ __device__ __forceinline__ int64_t load_expert(const void *experts, int64_t i)
 // the slots (segments ascend with r, then w).  Pass 1 counts the segment per
 // expert; the counts are turned into each warp's first row per expert (a scan
 // over warps, over blocks through distributed shared memory, and over
-// experts); pass 2 walks the segment again and places each slot.  Within 32
-// slots a match over the lanes gives the rank, so the order is the slots'.
+// experts); pass 2 places each slot: from its registers where the segment is no
+// longer than those hold, else walking it again.  Within 32 slots a match over
+// the lanes gives the rank, so the order is the slots'.
 template <typename I>
 __global__ void __launch_bounds__(1024)
 moe_plan_kernel(const void *__restrict__ experts, int64_t slots, int E, int C, int64_t seg,
@@ -71,9 +73,8 @@ moe_plan_kernel(const void *__restrict__ experts, int64_t slots, int E, int C, i
     const int64_t lo = (static_cast<int64_t>(rank) * warps + warp) * seg;
     const int64_t hi = lo + seg < slots ? lo + seg : slots;
     int32_t *mine = hist + warp * E;
-    // kKeys x 32 slots at a time: their loads are in flight together, and a
-    // segment no longer than that is read once for both passes
-    int key[kKeys];
+    // kKeys x 32 slots at a time: their loads are in flight together
+    int key[kKeys], place[kKeys];  // place: among the segment's slots of the same expert
     auto keys = [&](int64_t i0) {
         int64_t e[kKeys];
 #pragma unroll
@@ -95,7 +96,13 @@ moe_plan_kernel(const void *__restrict__ experts, int64_t slots, int E, int C, i
         for (int u = 0; u < kKeys; ++u) {
             if (i0 + 32 * u >= hi) break;
             const uint32_t peers = __match_any_sync(0xffffffffu, key[u]);
-            if (key[u] >= 0 && lane == __ffs(peers) - 1) mine[key[u]] += __popc(peers);
+            const int first = __ffs(peers) - 1;
+            int32_t seen = 0;
+            if (key[u] >= 0 && lane == first) {
+                seen = mine[key[u]];
+                mine[key[u]] = seen + __popc(peers);
+            }
+            place[u] = __shfl_sync(0xffffffffu, seen, first) + __popc(peers & ((1u << lane) - 1u));
             __syncwarp();
         }
     }
@@ -167,19 +174,27 @@ moe_plan_kernel(const void *__restrict__ experts, int64_t slots, int E, int C, i
     }
     __syncthreads();
 
-    for (int64_t i0 = lo; i0 < hi; i0 += 32 * kKeys) {
-        if (hi - lo > 32 * kKeys) keys(i0);
+    if (seg <= 32 * kKeys) {
 #pragma unroll
         for (int u = 0; u < kKeys; ++u) {
-            const int64_t i = i0 + 32 * u + lane;
-            if (i - lane >= hi) break;
-            const uint32_t peers = __match_any_sync(0xffffffffu, key[u]);
-            int32_t p = -1;
-            if (key[u] >= 0) p = base[key[u]] + mine[key[u]] + __popc(peers & ((1u << lane) - 1u));
-            __syncwarp();
-            if (key[u] >= 0 && lane == __ffs(peers) - 1) mine[key[u]] += __popc(peers);
-            __syncwarp();
-            if (i < hi) pos[i] = p;
+            const int64_t i = lo + 32 * u + lane;
+            if (i < hi) pos[i] = key[u] < 0 ? -1 : base[key[u]] + mine[key[u]] + place[u];
+        }
+    } else {
+        for (int64_t i0 = lo; i0 < hi; i0 += 32 * kKeys) {
+            keys(i0);
+    #pragma unroll
+            for (int u = 0; u < kKeys; ++u) {
+                const int64_t i = i0 + 32 * u + lane;
+                if (i - lane >= hi) break;
+                const uint32_t peers = __match_any_sync(0xffffffffu, key[u]);
+                int32_t p = -1;
+                if (key[u] >= 0) p = base[key[u]] + mine[key[u]] + __popc(peers & ((1u << lane) - 1u));
+                __syncwarp();
+                if (key[u] >= 0 && lane == __ffs(peers) - 1) mine[key[u]] += __popc(peers);
+                __syncwarp();
+                if (i < hi) pos[i] = p;
+            }
         }
     }
     if (C > 1) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
