@@ -27,7 +27,8 @@ def route(seed, T, k, E, drop=0.0, skew=False):
 
 @pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("T,k,E", [(1, 1, 1), (1, 8, 3), (5, 2, 8), (33, 3, 40), (300, 4, 64), (2048, 1, 7),
-                                   (2049, 1, 1024), (5000, 3, 16), (20000, 2, 128), (9000, 8, 1)])
+                                   (2049, 1, 1024), (5000, 3, 16), (20000, 2, 128), (9000, 8, 1), (8192, 8, 64),
+                                   (16384, 4, 1024), (30000, 3, 5)])
 @pytest.mark.parametrize("drop", [0.0, 0.4])
 def test_plan(T, k, E, drop, wide):
     e = route(T + E, T, k, E, drop, skew=T % 2 == 0)
