@@ -429,13 +429,17 @@ lowbit_status launch(const GsArgs &a, cudaStream_t st)
     if (ranges > fit) ranges = fit;
     if (ranges > runs) ranges = runs;
     // Two or three ranges: two warps of a block, without a cluster (12 tokens,
-    // 1280 -> 3584: 5.0 us against 6.2 for a cluster of three).  Six to eight: two
-    // in each block of a cluster of three or four (16 tokens, 4096 -> 512: 5.2
+    // 1280 -> 3584: 5.0 us against 6.2 for a cluster of three); the same where the
+    // row blocks alone are one per SM (four experts of 2048 -> 2048 with one row
+    // each: 6.6 against 8.9; 4 tokens, 5000 -> 6000: 9.9 against 12.5).  Six to eight:
+    // two in each block of a cluster of three or four (16 tokens, 4096 -> 512: 5.2
     // against 5.4 for eight blocks).  Else blocks only, in larger clusters but
     // with shorter ranges (4 tokens, 9728 -> 2560: 10.1 against 11.3; 8 tokens,
     // 2560 -> 2560: 6.3 against 6.9).
-    const int64_t kwarps = kMaxKWarps > 1 && ranges >= 2 && (ranges <= 3 || (ranges >= 6 && ranges <= 8)) ? kMaxKWarps : 1;
-    int64_t split = ranges / kwarps;
+    const bool full = kMaxKWarps > 1 && slabs * active >= device_sm_count();
+    const bool pair = ranges <= 3 || full || (ranges >= 6 && ranges <= 8);
+    const int64_t kwarps = kMaxKWarps > 1 && ranges >= 2 && pair ? kMaxKWarps : 1;
+    int64_t split = full ? 1 : ranges / kwarps;
     if (split < 1) split = 1;
     if (split > kMaxSplit) split = kMaxSplit;
     const int64_t per = (runs + split - 1) / split;
@@ -503,7 +507,10 @@ int64_t gs_mma_lanes(const GsArgs &a, int tok)
 lowbit_status gs_mma_launch(const GsArgs &a, cudaStream_t st)
 {
     const int64_t per = a.offsets != nullptr ? (a.M + a.E - 1) / a.E : a.M;
-    return per <= 8 ? gsm::launch_g<8>(a, st) : gsm::launch_g<16>(a, st);
+    // Experts with 6 rows on average often have more than 8, which would be two
+    // passes (16 experts of 1280 -> 3584 with 7 rows each: 19.0 against 18.4 us for
+    // passes of 16, with 8 rows 20.6; with 4 rows 15.4 against 18.2).
+    return per <= (a.offsets != nullptr ? 6 : 8) ? gsm::launch_g<8>(a, st) : gsm::launch_g<16>(a, st);
 }
 
 }  // namespace lowbit
